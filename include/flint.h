@@ -7,7 +7,11 @@
  *     caches;
  *   - prefill of a prompt (flint_prefill_qk_norm_rope, flint_prefill_attn);
  *   - context-parallel decode across GPUs (flint_attn_decode_partial,
- *     flint_merge_partials).
+ *     flint_merge_partials);
+ *   - speculative decode: drafted tokens normed and rotated at given positions
+ *     (flint_qk_norm_rope_at), their attention over the cache and their own
+ *     tree (flint_attn_tree), their verification (flint_verify_tree) and the
+ *     append of the accepted path (flint_kv_append_path).
  *
  * Model facts the operations follow (page title, section):
  *   - "Day-0 Support for Flint on vLLM" (hnkhoi.com/news/1467), "Model
@@ -67,6 +71,8 @@ extern "C" {
 #define FLINT_MAX_LAYERS 49       /* layers per flint_attn_stack call */
 #define FLINT_CP_PARTIAL_FLOATS 4160  /* 32*128 + 32 + 32: one context-parallel partial */
 #define FLINT_MAX_CP_PARTS 1024       /* partials per flint_merge_partials call */
+#define FLINT_MAX_TREE 64             /* drafted tokens per request of a speculative step */
+#define FLINT_MAX_VOCAB (1 << 24)     /* vocabulary size of flint_verify_tree */
 #define FLINT_NOALLOC_SCRATCH_BYTES (4u << 20)  /* flint_attn_stack_noalloc's fixed scratch */
 
 typedef enum {
@@ -373,6 +379,160 @@ flint_status flint_attn_decode_partial(const void* q, int32_t q_is_fp32,
  * partial and a sink of -inf (M = -inf) gets the output 0. */
 flint_status flint_merge_partials(const float* partials, int32_t n_parts, int32_t B,
                                   const float* sinks, float* out, void* stream);
+
+/* ---- speculative decode ------------------------------------------------------
+ * One step drafts up to FLINT_MAX_TREE tokens per request as a tree hung on the
+ * request's committed context of L_b tokens.  The tree is parent[b][i], the
+ * node that node i continues: -1 for the context itself, else an earlier node
+ * (parent[b][i] < i).  A node's depth d_i counts its ancestors, and it stands
+ * at position L_b + d_i.  Requests of a batch may hold fewer than N nodes
+ * (n_draft[b]); entries behind them are neither read as nodes nor written.  A
+ * parent outside [-1, i) counts as -1 and sets *dev_err =
+ * FLINT_ERR_INVALID_ARG.  The pages name no drafter; the definitions are those
+ * of speculative sampling with several drafted candidates per position. */
+
+typedef enum {
+    FLINT_ROPE_HALF = 0,         /* pairs (i, i + rotary_dim/2): the model's own form */
+    FLINT_ROPE_INTERLEAVED = 1   /* pairs (2i, 2i + 1) */
+} flint_rope_layout;
+
+typedef enum {
+    FLINT_ROPE_UNSCALED = 0,     /* f_i = theta^(-2i / rotary_dim) */
+    FLINT_ROPE_LINEAR = 1,       /* f_i / factor */
+    FLINT_ROPE_BY_PARTS = 2      /* with r_i = original_context f_i / (2 pi) turns over the
+                                    original context and g_i = (r_i - beta_slow) /
+                                    (beta_fast - beta_slow) clamped to [0, 1]:
+                                    g_i f_i + (1 - g_i) f_i / factor (the "NTK-by-parts"
+                                    interpolation of YaRN, arXiv 2309.00071) */
+} flint_rope_scaling;
+
+/* Rotary positions: the first rotary_dim dims of a head turn, pair i by the
+ * angle pos * f_i with cos and sin both times attn_factor; the rest pass. */
+typedef struct {
+    double theta;                /* > 0 */
+    double factor;               /* >= 1, finite */
+    double original_context;     /* BY_PARTS: > 0 */
+    double beta_fast, beta_slow; /* BY_PARTS: beta_fast > beta_slow >= 0 */
+    double attn_factor;          /* finite, > 0 */
+    int32_t rotary_dim;          /* even, 0 .. 128; 0 = no rotation */
+    int32_t layout;              /* flint_rope_layout */
+    int32_t scaling;             /* flint_rope_scaling */
+    int32_t reserved;            /* 0 */
+} flint_rope;
+
+/* One layer of flint_kv_append_path. */
+typedef struct {
+    const uint16_t* k;       /* bf16 [B][N][4][128]: the drafted k after norm/RoPE */
+    const uint16_t* v;       /* bf16 [B][N][4][128] */
+    flint_kv_cache cache;    /* this layer's cache (all B requests) */
+} flint_path_layer;
+
+/* Per-head Q/K RMSNorm and rotary positions of T tokens, each at a position of
+ * its own (flint_qk_norm_rope for any number of tokens, with positions on the
+ * device and other rotary forms).
+ *   q_raw  bf16, token t's row [32][128] at q_raw + t * q_stride elements;
+ *          k_raw bf16, [4][128] at k_raw + t * k_stride (device, in).  Strides:
+ *          multiples of 8, 0 = dense (4096 and 512); a projection's output that
+ *          holds q, k and v side by side is read in place
+ *   w_q, w_k  bf16 [128] norm weights, or both NULL: no norm
+ *   pos    device int32 [T], any values (outside [0, 2^31) none exist)
+ *   rope   host, or NULL: no rotation
+ *   q_out  bf16 [T][32][128], k_out bf16 [T][4][128] (device, out, dense):
+ *          rounded once to nearest even; either may be NULL (its input then
+ *          may be too).  An output may be its own input where that is dense.
+ * T in [0, FLINT_MAX_CONTEXT]; T = 0 does nothing.  Norm and rotation in
+ * float32, angles formed and reduced in double. */
+flint_status flint_qk_norm_rope_at(const uint16_t* q_raw, int64_t q_stride, const uint16_t* k_raw,
+                                   int64_t k_stride, const uint16_t* w_q, const uint16_t* w_k,
+                                   const int32_t* pos, int32_t T, float eps, const flint_rope* rope,
+                                   uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/* Bytes of device workspace for flint_attn_tree on num_ctas CTAs (0 = one per
+ * SM; they come in groups of four, at least one group): four partials of 66,560
+ * bytes per CTA.  It needs no initialisation and holds nothing between calls;
+ * calls that share one must not overlap in time.  0 for invalid arguments. */
+size_t flint_tree_workspace_bytes(int32_t num_ctas);
+
+/* Attention of drafted tokens over the committed cache and their own tree
+ * (flint_attn_decode for up to 64 tokens per request that are not in the cache
+ * yet).  Node i of request b attends the cached positions
+ * [max(0, L_b + d_i - window + 1), L_b) (window 513) or [0, L_b) (window 0),
+ * its ancestors and itself, with the head's sink:
+ *   out[b][i][h] = sum_j e^(s_j - M) V_j / (sum_j e^(s_j - M) + e^(sink_h - M)),
+ *   s_j = q[b][i][h] . K_j / sqrt(128), M = max(max_j s_j, sink_h).
+ * A chain (parent[i] = i - 1) gives what decoding its tokens one by one gives.
+ *   q         bf16 [B][N][32][128] (device, in), normed (and roped)
+ *   k_draft, v_draft  bf16 [B][N][4][128] (device, in), final; with an E4M3
+ *             cache they are attended as the cache would hold them (quantised
+ *             by its scales)
+ *   parent    device int32 [B][N]
+ *   seq_lens  HOST int32 [B]: committed tokens L_b, 0 <= L_b <=
+ *             FLINT_MAX_CONTEXT (and <= capacity, or the block table)
+ *   n_draft   HOST int32 [B]: nodes of each request, 0 <= n_draft[b] <= N
+ *   sinks     fp32 [32] (device); -INFINITY drops a sink
+ *   out       bf16 [B][N][32][128] (device): what the output projection reads,
+ *             rounded once; rows of nodes >= n_draft[b] are left as they were
+ *   workspace device, >= flint_tree_workspace_bytes(num_ctas)
+ * N in [1, FLINT_MAX_TREE], B in [1, FLINT_MAX_BATCH].  Scores and sums are
+ * fp32; the probabilities and v enter their product in fp16 (v saturating at
+ * +-65504, exact for bf16 values in the fp16 normal range, as in the
+ * prefill), and with an E4M3 cache q in fp16 too.  Cache slots outside the
+ * attended range may hold anything.  Results are the same run to run for
+ * given lengths, N and num_ctas.  Paged block ids and time-outs as for
+ * flint_attn_decode. */
+flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const uint16_t* v_draft,
+                             const int32_t* parent, int32_t N, const flint_kv_cache* cache,
+                             const int32_t* seq_lens, const int32_t* n_draft, int32_t B,
+                             const float* sinks, int32_t window, uint16_t* out, void* workspace,
+                             size_t ws_bytes, int32_t num_ctas, int32_t* dev_err, void* stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers: the longest path of the tree that speculative sampling
+ * accepts, and the token that follows it, distributed as the target's own
+ * samples.  Per request, from the context (cur = -1) with w = target row 0 and
+ * Z = 1, over the nodes i in order whose parent is cur, with x = tokens[i]:
+ *     accepted  if  u_accept[i] * q(x) * Z < w(x):  cur = i, w = target row i + 1, Z = 1;
+ *     rejected  otherwise:  w = max(w - Z q, 0), Z = sum(w)  (unless that sum is 0).
+ * q is draft row parent[i] + 1, from which the children of that node were
+ * drawn independently; with draft = NULL the candidates are fixed ones (q = 1
+ * at x): w(x) = 0 and Z = Z - w(x).  Then next_token is the smallest y with
+ * sum_{z <= y} w(z) > u_sample * sum(w) (the last y with w(y) > 0 where
+ * rounding leaves none, 0 where w is 0 everywhere).
+ *   target  fp32, row r of request b at target + (b (N + 1) + r) * target_stride
+ *           elements, r in [0, N] (0: after the context, i + 1: after node i);
+ *           each sums to 1 (device, in)
+ *   draft   fp32, row r at draft + (b N + r) * draft_stride, r in [0, N), or NULL
+ *   V       row length, in [1, FLINT_MAX_VOCAB]; strides >= V, 0 = V
+ *   tokens, parent  device int32 [B][N]; a token outside [0, V) is rejected
+ *           without touching w and sets *dev_err = FLINT_ERR_INVALID_ARG
+ *   n_draft HOST int32 [B], 0 <= n_draft[b] <= N
+ *   u_accept fp32 [B][N], u_sample fp32 [B] in [0, 1) (device, in)
+ *   path    device int32 [B][N] (out): the accepted nodes in order, then -1
+ *   n_accepted, next_token  device int32 [B] (out)
+ * N in [1, FLINT_MAX_TREE], B in [1, FLINT_MAX_BATCH].  All arithmetic in
+ * double: a draw that decides at a border decides as the formula does. */
+flint_status flint_verify_tree(const float* target, int64_t target_stride, const float* draft,
+                               int64_t draft_stride, const int32_t* tokens, const int32_t* parent,
+                               const int32_t* n_draft, int32_t B, int32_t N, int32_t V,
+                               const float* u_accept, const float* u_sample, int32_t* path,
+                               int32_t* n_accepted, int32_t* next_token, int32_t* dev_err,
+                               void* stream);
+
+/* Append of the accepted path to every layer's cache in one launch
+ * (flint_kv_append for the tokens that flint_verify_tree accepted): the
+ * drafted k and v of node path[b][j] go to position L_b + j, j <
+ * n_accepted[b], of each layer's cache (E4M3 caches: quantised as
+ * flint_kv_append does).  Other slots are not written.
+ *   layers  HOST array [n_layers], 1 <= n_layers <= FLINT_MAX_LAYERS
+ *   path    device int32 [B][N], n_accepted device int32 [B]
+ *   seq_lens  HOST int32 [B]: L_b, 0 <= L_b <= FLINT_MAX_CONTEXT
+ * A count outside [0, N], a node outside [0, N), a position outside the cache
+ * or the block table, or a paged block id out of range writes nothing for
+ * that token and sets *dev_err = FLINT_ERR_INVALID_ARG. */
+flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_layers,
+                                  const int32_t* path, const int32_t* n_accepted, int32_t N,
+                                  const int32_t* seq_lens, int32_t B, int32_t* dev_err,
+                                  void* stream);
 
 /* The split planner behind both attention calls (pure host code, exposed for
  * tests).  Work is n_segs segments (one per problem, all four KV heads

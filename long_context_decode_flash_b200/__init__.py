@@ -10,6 +10,7 @@ _BINDING_NAMES = (
     "flint_attn_workspace_bytes", "flint_attn_decode", "flint_attn_stack",
     "flint_attn_stack_noalloc", "flint_attn_layers_serial",
     "flint_plan_items", "flint_plan_split", "KVCache", "StackLayer",
+    "flint_qk_norm_rope_at", "flint_attn_tree", "flint_verify_tree", "flint_kv_append_path",
 )
 
 __all__ = list(_BINDING_NAMES) + ["inputs"]

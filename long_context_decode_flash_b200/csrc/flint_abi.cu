@@ -38,11 +38,13 @@ flint_status ok() {
   return FLINT_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 constexpr int kItemCost = 2;  // per-item overhead in tile units (planner cost model)
 
+}  // namespace
+
 // ---- device properties (cached per device) --------------------------------
+
+namespace flint {
 
 int device_num_sms(int* out) {
   static std::mutex mu;
@@ -62,11 +64,6 @@ int device_num_sms(int* out) {
 
 // ---- TMA tensor maps --------------------------------------------------------
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -80,6 +77,10 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+}  // namespace flint
+
+namespace {
 
 // Encoded maps are kept per (device, base, geometry): a decode loop calls with
 // the same caches every token, so encoding happens once.
@@ -157,7 +158,11 @@ flint_status encode_cache_map(CUtensorMap* map, void* base, const flint_kv_cache
   return FLINT_OK;
 }
 
+}  // namespace
+
 // ---- validation -------------------------------------------------------------
+
+namespace flint {
 
 flint_status check_cache(const flint_kv_cache* c, int B, const char* who) {
   if (!c) return fail(FLINT_ERR_INVALID_ARG, "%s: cache is NULL", who);
@@ -196,6 +201,10 @@ flint_status check_cache(const flint_kv_cache* c, int B, const char* who) {
       return fail(FLINT_ERR_INVALID_ARG, "%s: unknown cache layout %d", who, c->layout);
   }
 }
+
+}  // namespace flint
+
+namespace {
 
 // Attended range of one request in storage coordinates, plus its tiles.
 struct Range {
@@ -488,6 +497,8 @@ flint_status record_error(flint_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+
+flint_status record_ok() { return ok(); }
 
 }  // namespace flint
 

@@ -253,6 +253,21 @@ size_t workspace_min_bytes(int n_problems, int num_ctas);
 // Sets the message that flint_last_error() returns on this thread; returns s.
 flint_status record_error(flint_status s, const char* fmt, ...);
 
+// Clears that message; returns FLINT_OK.
+flint_status record_ok();
+
+// Host-side checks and look-ups shared by the entry points.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int device_num_sms(int* out);  // SMs of the current device; 0 = found
+flint_status check_cache(const flint_kv_cache* c, int B, const char* who);
+
+// The driver's tensor-map encoder, or nullptr.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // The CUDA context current on the calling thread (a driver handle), or
 // nullptr if there is none yet.  Per-context state (a kernel's shared-memory
 // attribute, the address of a module variable) is keyed on it: after a device

@@ -1,0 +1,98 @@
+// flint_spec.h -- kernel parameters and launchers of the speculative-decode
+// calls (tree attention, verification, norm and rotary at given positions,
+// append of an accepted path).
+#pragma once
+
+#include "flint_internal.h"
+
+namespace flint {
+
+constexpr int kMaxTree = FLINT_MAX_TREE;
+
+// ---- flint_qk_norm_rope_at ----------------------------------------------------
+struct RopeAtParams {
+  const uint16_t* q_raw;     // or nullptr: no q rows
+  const uint16_t* k_raw;     // or nullptr: no k rows
+  int64_t q_stride, k_stride;  // elements between tokens
+  const uint16_t* w_q;       // nullptr: no norm
+  const uint16_t* w_k;
+  const int32_t* pos;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int32_t T;
+  int32_t rotary_dim;        // 0: no rotation
+  int32_t layout;            // flint_rope_layout
+  float eps;
+  float attn_factor;
+  double turns[kDim / 2];    // f_i / (2 pi): a pair's turns per position
+};
+cudaError_t launch_rope_at(const RopeAtParams& p, int num_sms, cudaStream_t stream);
+
+// ---- flint_kv_append_path -------------------------------------------------------
+struct PathLayer {
+  const uint16_t* k;
+  const uint16_t* v;
+  uint8_t* k_rows;           // the cache's buffers
+  uint8_t* v_rows;
+  const int32_t* table;
+  int64_t req_stride;        // elements
+  int32_t layout, capacity, max_blocks, num_blocks, fp8;
+  float k_scale[4], v_scale[4];
+};
+struct AppendPathParams {
+  PathLayer layer[FLINT_MAX_LAYERS];
+  int32_t len[FLINT_MAX_BATCH];
+  const int32_t* path;
+  const int32_t* n_accepted;
+  int32_t* dev_err;
+  int32_t n_layers, N, B;
+};
+static_assert(sizeof(AppendPathParams) <= 32000, "kernel parameters exceed 32 KiB");
+cudaError_t launch_append_path(const AppendPathParams& p, cudaStream_t stream);
+
+// ---- flint_verify_tree ------------------------------------------------------------
+struct VerifyParams {
+  const float* target;
+  const float* draft;        // or nullptr: fixed candidates
+  int64_t target_stride, draft_stride;
+  const int32_t* tokens;
+  const int32_t* parent;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* path;
+  int32_t* n_accepted;
+  int32_t* next_token;
+  int32_t* dev_err;
+  int32_t B, N, V;
+  int8_t n_draft[FLINT_MAX_BATCH];
+};
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
+
+// ---- flint_attn_tree ----------------------------------------------------------------
+// A partial: O of 128 rows (16 nodes x 8 heads), m and l, fp32.  A CTA may leave
+// two items unfinished (its first and its last) of up to two partials each, and
+// CTAs come in groups of four, one per KV head.
+constexpr int kTreePartialFloats = 128 * kDim + 2 * 128;
+constexpr size_t kTreeGroupBytes = size_t(kKvHeads) * 2 * 2 * kTreePartialFloats * 4;
+
+struct TreeParams {
+  const uint16_t* q;
+  const uint16_t* k_draft;
+  const uint16_t* v_draft;
+  const int32_t* parent;
+  const float* sinks;
+  uint16_t* out;
+  const uint8_t* k_rows;     // the cache's buffers
+  const uint8_t* v_rows;
+  const int32_t* table;
+  int64_t req_stride;        // elements
+  int32_t layout, capacity, max_blocks, num_blocks, fp8;
+  float k_scale[4], v_scale[4];
+  int32_t len[FLINT_MAX_BATCH];
+  int8_t n_draft[FLINT_MAX_BATCH];
+  int32_t N, B, window;
+  int32_t* dev_err;
+};
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
+
+}  // namespace flint

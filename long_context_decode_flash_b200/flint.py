@@ -7,6 +7,7 @@ no fallback: if libflint.so is missing or a call fails, FlintError is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Sequence
@@ -34,8 +35,12 @@ EXPORTED = (
     "flint_kv_append", "flint_attn_workspace_bytes", "flint_attn_decode", "flint_attn_stack",
     "flint_attn_stack_noalloc", "flint_attn_layers_serial", "flint_plan_items", "flint_plan_split",
     "flint_prefill_qk_norm_rope", "flint_prefill_attn", "flint_attn_decode_partial",
-    "flint_merge_partials",
+    "flint_merge_partials", "flint_qk_norm_rope_at", "flint_tree_workspace_bytes", "flint_attn_tree",
+    "flint_verify_tree", "flint_kv_append_path",
 )
+MAX_TREE = 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_UNSCALED, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
 CP_PARTIAL_FLOATS = 32 * 128 + 2 * 32
 
 
@@ -60,6 +65,19 @@ class StackLayer(ctypes.Structure):
     _fields_ = [("q_raw", ctypes.c_void_p), ("k_raw", ctypes.c_void_p), ("v_raw", ctypes.c_void_p),
                 ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("sinks", ctypes.c_void_p),
                 ("cache", KVCache), ("window", ctypes.c_int32), ("rope", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """flint_rope.  Build with rope()."""
+    _fields_ = [("theta", ctypes.c_double), ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("attn_factor", ctypes.c_double),
+                ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class PathLayer(ctypes.Structure):
+    """flint_path_layer."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("cache", KVCache)]
 
 
 _lock = threading.Lock()
@@ -98,6 +116,12 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.flint_prefill_attn.argtypes = [P, P, P, I32, P, I32, P, P, P]
     lib.flint_attn_decode_partial.argtypes = [P, I32, P, P, I32, P, P, ctypes.c_size_t, I32, P, P]
     lib.flint_merge_partials.argtypes = [P, I32, I32, P, P, P]
+    lib.flint_qk_norm_rope_at.argtypes = [P, I64, P, I64, P, P, P, I32, ctypes.c_float, P, P, P, P]
+    lib.flint_tree_workspace_bytes.argtypes = [I32]
+    lib.flint_tree_workspace_bytes.restype = ctypes.c_size_t
+    lib.flint_attn_tree.argtypes = [P, P, P, P, I32, P, P, P, I32, P, I32, P, P, ctypes.c_size_t, I32, P, P]
+    lib.flint_verify_tree.argtypes = [P, I64, P, I64, P, P, P, I32, I32, I32, P, P, P, P, P, P, P]
+    lib.flint_kv_append_path.argtypes = [P, I32, P, P, I32, P, I32, P, P]
     lib.flint_plan_items.argtypes = [P, I32, I32, I32, P, P, P, P, I32]
     lib.flint_plan_items.restype = I32
     lib.flint_plan_split.argtypes = [P, I32, I32, I32, I32, P, P, P, P, P]
@@ -105,7 +129,8 @@ def open_library(path: str) -> ctypes.CDLL:
     for name in ("flint_qk_norm_rope", "flint_kv_append", "flint_attn_decode",
                  "flint_attn_stack", "flint_attn_stack_noalloc", "flint_attn_layers_serial",
                  "flint_prefill_qk_norm_rope", "flint_prefill_attn", "flint_attn_decode_partial",
-                 "flint_merge_partials"):
+                 "flint_merge_partials", "flint_qk_norm_rope_at", "flint_attn_tree", "flint_verify_tree",
+                 "flint_kv_append_path"):
         getattr(lib, name).restype = ctypes.c_int
     # test builds only (libflint_hooks.so): leave one pipeline stage unarmed
     for name in ("flint_test_stall_decode", "flint_test_stall_prefill", "flint_test_stall_prefill_prep"):
@@ -329,6 +354,171 @@ def flint_attn_stack_noalloc(layers, pos: int, out, eps: float = 1e-6, theta: fl
     _check(lib.flint_attn_stack_noalloc(arr, len(arr), int(pos), eps, theta, _ptr(out),
                                         int(num_ctas), _ptr(dev_err), _stream(stream)))
     return out
+
+
+# ---- speculative decode ------------------------------------------------------
+
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise FlintError(FLINT_ERR_INVALID_ARG, what)
+
+
+def _dense(t, dtype, shape, name: str) -> None:
+    """A dense tensor of this type and shape on the current device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be a dense {dtype} tensor {list(shape)}, "
+                         f"not {t.dtype} {list(t.shape)}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def rope(rotary_dim: int = HEAD_DIM, interleaved: bool = False, theta: float = 10000.0, scaling: str = "none",
+         factor: float = 1.0, original_context: float = 8192.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+         attn_factor: Optional[float] = None) -> Rope:
+    """A flint_rope: the first `rotary_dim` dims turn, in pairs (i, i + rotary_dim/2)
+    or (2i, 2i + 1) (interleaved); scaling "none", "linear" (every frequency over
+    `factor`) or "yarn" (by parts).  attn_factor multiplies cos and sin; by
+    default 1, with "yarn" 0.1 ln(factor) + 1."""
+    kinds = {"none": ROPE_UNSCALED, "linear": ROPE_LINEAR, "yarn": ROPE_BY_PARTS}
+    _need(scaling in kinds, f"unknown rotary scaling {scaling!r}")
+    if attn_factor is None:
+        attn_factor = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor >= 1.0 else 1.0
+    return Rope(theta, factor, original_context, beta_fast, beta_slow, attn_factor, int(rotary_dim),
+                ROPE_INTERLEAVED if interleaved else ROPE_HALF, kinds[scaling], 0)
+
+
+def _token_rows(t, heads: int, T: int, name: str) -> int:
+    """The token stride (elements) of bf16 [T, heads, 128] with dense heads."""
+    if (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, HEAD_DIM) or t.device.type != "cuda"
+            or t.device.index != torch.cuda.current_device()):
+        raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be bf16 [{T}, {heads}, 128] on the current CUDA device")
+    st = t.stride()
+    _need(T == 0 or st[2] == 1 and st[1] == HEAD_DIM and (T == 1 or st[0] >= heads * HEAD_DIM),
+          f"{name}: the heads of a token must be dense, and the tokens apart")
+    return st[0] if T > 1 else 0
+
+
+def flint_qk_norm_rope_at(q_raw, k_raw, w_q, w_k, pos, rope: Optional[Rope] = None, eps: float = 1e-6, q_out=None,
+                          k_out=None, stream=None):
+    """RMSNorm (unless w_q and w_k are None) and rotary positions of T tokens at
+    the positions pos (device int32 [T]): q_raw [T, 32, 128] and k_raw
+    [T, 4, 128] in bf16, dense or slices of wider token rows, to the dense
+    q_out and k_out."""
+    T = int(pos.shape[0])
+    _dense(pos, torch.int32, (T,), "pos")
+    qs = _token_rows(q_raw, NUM_Q_HEADS, T, "q_raw") if q_out is not None else 0
+    ks = _token_rows(k_raw, NUM_KV_HEADS, T, "k_raw") if k_out is not None else 0
+    if q_out is not None:
+        _dense(q_out, torch.bfloat16, (T, NUM_Q_HEADS, HEAD_DIM), "q_out")
+    if k_out is not None:
+        _dense(k_out, torch.bfloat16, (T, NUM_KV_HEADS, HEAD_DIM), "k_out")
+    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None:
+            _dense(w, torch.bfloat16, (HEAD_DIM,), name)
+    _check(load_library().flint_qk_norm_rope_at(
+        _ptr(q_raw), qs, _ptr(k_raw), ks, _ptr(w_q), _ptr(w_k), _ptr(pos), T, eps,
+        ctypes.byref(rope) if rope is not None else None, _ptr(q_out), _ptr(k_out), _stream(stream)))
+    return q_out, k_out
+
+
+def flint_tree_workspace_bytes(num_ctas: int = 0) -> int:
+    return int(load_library().flint_tree_workspace_bytes(num_ctas))
+
+
+def tree_workspace(num_ctas: int = 0, device=None) -> torch.Tensor:
+    """A workspace for flint_attn_tree (uninitialised: it needs no zeroing)."""
+    n = flint_tree_workspace_bytes(num_ctas)
+    _need(n > 0, "invalid workspace request")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def flint_attn_tree(q, k_draft, v_draft, parent, cache: KVCache, seq_lens: Sequence[int], n_draft: Sequence[int], sinks,
+                    window: int, out, ws: torch.Tensor, num_ctas: int = 0, dev_err=None, stream=None):
+    """Attention of drafted tokens [B, N] over the cache and their own tree: q and
+    out bf16 [B, N, 32, 128], k_draft and v_draft bf16 [B, N, 4, 128], parent
+    int32 [B, N]; seq_lens and n_draft are host values per request."""
+    _need(q.dim() == 4, "q must be [B, N, 32, 128]")
+    B, N = int(q.shape[0]), int(q.shape[1])
+    _dense(q, torch.bfloat16, (B, N, NUM_Q_HEADS, HEAD_DIM), "q")
+    _dense(k_draft, torch.bfloat16, (B, N, NUM_KV_HEADS, HEAD_DIM), "k_draft")
+    _dense(v_draft, torch.bfloat16, (B, N, NUM_KV_HEADS, HEAD_DIM), "v_draft")
+    _dense(parent, torch.int32, (B, N), "parent")
+    _dense(sinks, torch.float32, (NUM_Q_HEADS,), "sinks")
+    _dense(out, torch.bfloat16, (B, N, NUM_Q_HEADS, HEAD_DIM), "out")
+    _need(len(seq_lens) == B and len(n_draft) == B, f"seq_lens and n_draft must hold {B} values")
+    _check(load_library().flint_attn_tree(
+        _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(parent), N, ctypes.byref(cache), _i32_host(seq_lens),
+        _i32_host(n_draft), B, _ptr(sinks), int(window), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+        int(num_ctas), _ptr(dev_err), _stream(stream)))
+    return out
+
+
+def _prob_rows(t, B: int, rows: int, name: str) -> int:
+    """The row stride (elements) of fp32 [B, rows, V] whose rows are evenly spaced."""
+    if (t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != rows or t.device.type != "cuda"
+            or t.device.index != torch.cuda.current_device()):
+        raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be fp32 [{B}, {rows}, V] on the current CUDA device")
+    b, r, v = t.stride()
+    if rows == 1:
+        r = b if B > 1 else t.shape[2]
+    _need((v == 1 or t.shape[2] == 1) and (B == 1 or b == rows * r) and r >= t.shape[2],
+          f"{name}: rows must be dense, apart and evenly spaced over the batch")
+    return r
+
+
+def flint_verify_tree(target, draft, tokens, parent, n_draft: Sequence[int], u_accept, u_sample, path, n_accepted,
+                      next_token, dev_err=None, stream=None):
+    """Verification of drafted tokens [B, N] against the target's probabilities
+    fp32 [B, N + 1, V] (row 0 after the context, row i + 1 after node i), from
+    the uniforms u_accept [B, N] and u_sample [B]; draft fp32 [B, N, V] holds the
+    distributions that the children of each row's node were drawn from, None:
+    fixed candidates.  Writes path int32 [B, N], n_accepted and next_token int32 [B]."""
+    B, N = int(tokens.shape[0]), int(tokens.shape[1])
+    ts = _prob_rows(target, B, N + 1, "target")
+    V = int(target.shape[2])
+    ds = 0
+    if draft is not None:
+        ds = _prob_rows(draft, B, N, "draft")
+        _need(int(draft.shape[2]) == V, "target and draft must have rows of one length")
+    for t, dtype, shape, name in ((tokens, torch.int32, (B, N), "tokens"), (parent, torch.int32, (B, N), "parent"),
+                                  (u_accept, torch.float32, (B, N), "u_accept"), (u_sample, torch.float32, (B,), "u_sample"),
+                                  (path, torch.int32, (B, N), "path"), (n_accepted, torch.int32, (B,), "n_accepted"),
+                                  (next_token, torch.int32, (B,), "next_token")):
+        _dense(t, dtype, shape, name)
+    _need(len(n_draft) == B, f"n_draft must hold {B} values")
+    _check(load_library().flint_verify_tree(
+        _ptr(target), ts, _ptr(draft), ds, _ptr(tokens), _ptr(parent), _i32_host(n_draft), B, N, V, _ptr(u_accept),
+        _ptr(u_sample), _ptr(path), _ptr(n_accepted), _ptr(next_token), _ptr(dev_err), _stream(stream)))
+    return path, n_accepted, next_token
+
+
+def path_layers(layers) -> ctypes.Array:
+    """A flint_path_layer array from (k_draft, v_draft, cache) per layer: bf16
+    [B, N, 4, 128] tensors and the layer's KVCache."""
+    arr = (PathLayer * len(layers))()
+    shape = tuple(layers[0][0].shape) if len(layers) else ()
+    for i, (k, v, cache) in enumerate(layers):
+        for t, name in ((k, "k"), (v, "v")):
+            _need(len(shape) == 4, "the drafts must be [B, N, 4, 128]")
+            _dense(t, torch.bfloat16, shape[:2] + (NUM_KV_HEADS, HEAD_DIM), f"layer {i}: {name}")
+        arr[i].k, arr[i].v, arr[i].cache = k.data_ptr(), v.data_ptr(), cache
+    arr._keep, arr._shape = list(layers), shape[:2]
+    return arr
+
+
+def flint_kv_append_path(layers, path, n_accepted, seq_lens: Sequence[int], dev_err=None, stream=None) -> None:
+    """Append the drafted k and v of the accepted nodes path[b, :n_accepted[b]]
+    (device int32) at positions seq_lens[b] .. of every layer's cache; layers:
+    an array from path_layers() or a list for it."""
+    arr = layers if isinstance(layers, ctypes.Array) else path_layers(layers)
+    _need(len(arr) > 0 and path.dim() == 2 and tuple(path.shape) == arr._shape, "path must be [B, N] as the layers' drafts are")
+    B, N = int(path.shape[0]), int(path.shape[1])
+    _dense(path, torch.int32, (B, N), "path")
+    _dense(n_accepted, torch.int32, (B,), "n_accepted")
+    _need(len(seq_lens) == B, f"seq_lens must hold {B} values")
+    _check(load_library().flint_kv_append_path(arr, len(arr), _ptr(path), _ptr(n_accepted), N, _i32_host(seq_lens), B,
+                                               _ptr(dev_err), _stream(stream)))
 
 
 def flint_plan_items(seg_tiles: Sequence[int], num_ctas: int, item_cost: int = 2,
