@@ -75,24 +75,49 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
 constexpr int kTreePartialFloats = 128 * kDim + 2 * 128;
 constexpr size_t kTreeGroupBytes = size_t(kKvHeads) * 2 * 2 * kTreePartialFloats * 4;
 
+// A unit: up to 32 nodes of a request (mt row tiles of 16) against its keys, in
+// tiles of two 64-key halves: half 0 the drafted tokens, half h >= 1 the cache's
+// storage rows (positions; slots of a ring) base + 64 (h - 1) .., of which
+// [lo, hi) hold tokens that some node attends.
+constexpr int kMaxTreeUnits = FLINT_MAX_BATCH * (kMaxTree / 32);
+struct TreeUnit {
+  int16_t b;
+  int8_t rb, mt;
+  int32_t base, lo, hi;
+  int32_t halves, tiles;
+  int16_t q0, q1;            // the groups that hold a share of it
+};
+struct TreeCut {
+  int16_t unit, tile;
+};
+constexpr int kMaxTreeGroups = kMaxCtas / kKvHeads;
+
 struct TreeParams {
+  // [128 dims][4 heads][capacity | 64 tokens][B | num_blocks], 128-byte swizzle,
+  // boxes of 64 tokens x 128 bytes (64 dims bf16, 128 dims E4M3)
+  CUtensorMap k_map, v_map;
   const uint16_t* q;
   const uint16_t* k_draft;
   const uint16_t* v_draft;
   const int32_t* parent;
   const float* sinks;
   uint16_t* out;
-  const uint8_t* k_rows;     // the cache's buffers
-  const uint8_t* v_rows;
+  float* partials;
   const int32_t* table;
-  int64_t req_stride;        // elements
-  int32_t layout, capacity, max_blocks, num_blocks, fp8;
+  int32_t layout, max_blocks, num_blocks, fp8;
   float k_scale[4], v_scale[4];
   int32_t len[FLINT_MAX_BATCH];
   int8_t n_draft[FLINT_MAX_BATCH];
   int32_t N, B, window;
+  int32_t n_units, n_groups, split;  // split: some unit is shared by groups
+  TreeUnit unit[kMaxTreeUnits];
+  TreeCut cut[kMaxTreeGroups + 1];   // group q: from cut[q] to cut[q + 1]
   int32_t* dev_err;
 };
+static_assert(sizeof(TreeParams) <= 32000, "kernel parameters exceed 32 KiB");
+// Fills unit, cut, n_units, n_groups and split from len, n_draft, B, window,
+// layout and fp8, for at most num_groups groups of CTAs.
+void plan_tree(TreeParams& p, int num_groups);
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
 
 }  // namespace flint

@@ -77,6 +77,25 @@ flint_status rope_turns(const flint_rope* r, RopeAtParams* p, const char* who) {
   return FLINT_OK;
 }
 
+// A cache buffer as the tree attention reads it (TreeParams::k_map).
+flint_status tree_map(CUtensorMap* map, void* base, const flint_kv_cache& c, int B, const char* who) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return record_error(FLINT_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available from the driver", who);
+  const bool fp8 = c.dtype == FLINT_KV_FP8_E4M3, paged = c.layout == FLINT_KV_PAGED;
+  const cuuint64_t eb = fp8 ? 1 : 2;
+  const cuuint64_t dims[4] = {kDim, kKvHeads, static_cast<cuuint64_t>(paged ? kBlock : c.capacity),
+                              static_cast<cuuint64_t>(paged ? c.num_blocks : B)};
+  const cuuint64_t apart = paged ? static_cast<cuuint64_t>(kBlock) * kKvHeads * kDim : static_cast<cuuint64_t>(request_stride(c));
+  const cuuint64_t strides[3] = {kDim * eb, kKvHeads * kDim * eb, apart * eb};
+  const cuuint32_t box[4] = {fp8 ? 128u : 64u, 1, 64, 1};
+  const cuuint32_t each[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+                        each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        static_cast<CUtensorMapL2promotion>(FLINT_L2_PROMOTION), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return record_error(FLINT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (CUresult %d)", who, static_cast<int>(r));
+  return FLINT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -174,12 +193,9 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   p.parent = parent;
   p.sinks = sinks;
   p.out = out;
-  p.k_rows = static_cast<const uint8_t*>(c.k);
-  p.v_rows = static_cast<const uint8_t*>(c.v);
+  p.partials = static_cast<float*>(workspace);
   p.table = c.block_table;
-  p.req_stride = request_stride(c);
   p.layout = c.layout;
-  p.capacity = c.capacity;
   p.max_blocks = c.max_blocks_per_req;
   p.num_blocks = c.num_blocks;
   p.fp8 = c.dtype == FLINT_KV_FP8_E4M3;
@@ -191,6 +207,13 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   p.B = B;
   p.window = window;
   p.dev_err = dev_err;
+  int sms = kMaxCtas;
+  if (num_ctas == 0 && device_num_sms(&sms) != 0) return record_error(FLINT_ERR_CUDA, "%s: cannot read the device's SM count", who);
+  plan_tree(p, std::max(1, (num_ctas ? num_ctas : sms) / kKvHeads));
+  if (p.n_units == 0) return record_ok();
+  s = tree_map(&p.k_map, c.k, c, B, who);
+  if (s == FLINT_OK) s = tree_map(&p.v_map, c.v, c, B, who);
+  if (s != FLINT_OK) return s;
   return launched(launch_tree(p, static_cast<cudaStream_t>(stream)), who);
 }
 
