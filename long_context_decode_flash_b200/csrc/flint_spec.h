@@ -83,6 +83,7 @@ constexpr int kMaxTreeUnits = FLINT_MAX_BATCH * (kMaxTree / 32);
 struct TreeUnit {
   int16_t b;
   int8_t rb, mt;
+  int8_t dup;                // copies of the rows in the row tile
   int32_t base, lo, hi;
   int32_t halves, tiles;
   int16_t q0, q1;            // the groups that hold a share of it
@@ -96,9 +97,9 @@ struct TreeParams {
   // [128 dims][4 heads][capacity | 64 tokens][B | num_blocks], 128-byte swizzle,
   // boxes of 64 tokens x 128 bytes (64 dims bf16, 128 dims E4M3)
   CUtensorMap k_map, v_map;
-  const uint16_t* q;
-  const uint16_t* k_draft;
-  const uint16_t* v_draft;
+  // [128 dims][32 | 4 heads][B * N nodes] bf16, boxes of 64 dims: 8 heads x 8
+  // nodes, 1 head x 64 nodes
+  CUtensorMap q_map, kd_map, vd_map;
   const int32_t* parent;
   const float* sinks;
   uint16_t* out;
@@ -109,7 +110,7 @@ struct TreeParams {
   int32_t len[FLINT_MAX_BATCH];
   int8_t n_draft[FLINT_MAX_BATCH];
   int32_t N, B, window;
-  int32_t n_units, n_groups, split;  // split: some unit is shared by groups
+  int32_t n_units, n_groups, split;  // split: some unit leaves partials
   TreeUnit unit[kMaxTreeUnits];
   TreeCut cut[kMaxTreeGroups + 1];   // group q: from cut[q] to cut[q + 1]
   int32_t* dev_err;

@@ -77,23 +77,34 @@ flint_status rope_turns(const flint_rope* r, RopeAtParams* p, const char* who) {
   return FLINT_OK;
 }
 
-// A cache buffer as the tree attention reads it (TreeParams::k_map).
-flint_status tree_map(CUtensorMap* map, void* base, const flint_kv_cache& c, int B, const char* who) {
+// A 4-D tensor map (128-byte swizzle) of rows of 128 dims: 64 bf16 or 128 E4M3
+// values wide boxes of box1 x box2 rows.
+flint_status encode_map(CUtensorMap* map, const void* base, bool fp8, const cuuint64_t (&dims)[4], const cuuint64_t (&apart)[3],
+                        cuuint32_t box1, cuuint32_t box2, const char* who) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return record_error(FLINT_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available from the driver", who);
-  const bool fp8 = c.dtype == FLINT_KV_FP8_E4M3, paged = c.layout == FLINT_KV_PAGED;
-  const cuuint64_t eb = fp8 ? 1 : 2;
-  const cuuint64_t dims[4] = {kDim, kKvHeads, static_cast<cuuint64_t>(paged ? kBlock : c.capacity),
-                              static_cast<cuuint64_t>(paged ? c.num_blocks : B)};
-  const cuuint64_t apart = paged ? static_cast<cuuint64_t>(kBlock) * kKvHeads * kDim : static_cast<cuuint64_t>(request_stride(c));
-  const cuuint64_t strides[3] = {kDim * eb, kKvHeads * kDim * eb, apart * eb};
-  const cuuint32_t box[4] = {fp8 ? 128u : 64u, 1, 64, 1};
-  const cuuint32_t each[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
-                        each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint64_t eb = fp8 ? 1 : 2, strides[3] = {apart[0] * eb, apart[1] * eb, apart[2] * eb};
+  const cuuint32_t box[4] = {fp8 ? 128u : 64u, box1, box2, 1}, each[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+                        dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         static_cast<CUtensorMapL2promotion>(FLINT_L2_PROMOTION), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return record_error(FLINT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (CUresult %d)", who, static_cast<int>(r));
   return FLINT_OK;
+}
+
+// A cache buffer, and q or a draft, as the tree attention reads them
+// (TreeParams).
+flint_status tree_map(CUtensorMap* map, const void* base, const flint_kv_cache& c, int B, const char* who) {
+  const bool paged = c.layout == FLINT_KV_PAGED;
+  const cuuint64_t request = paged ? static_cast<cuuint64_t>(kBlock) * kKvHeads * kDim : static_cast<cuuint64_t>(request_stride(c));
+  return encode_map(map, base, c.dtype == FLINT_KV_FP8_E4M3,
+                    {kDim, kKvHeads, static_cast<cuuint64_t>(paged ? kBlock : c.capacity), static_cast<cuuint64_t>(paged ? c.num_blocks : B)},
+                    {kDim, kKvHeads * kDim, request}, 1, 64, who);
+}
+flint_status rows_map(CUtensorMap* map, const void* base, int heads, int rows, cuuint32_t box1, cuuint32_t box2, const char* who) {
+  const cuuint64_t row = static_cast<cuuint64_t>(heads) * kDim;
+  return encode_map(map, base, false, {kDim, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows), 1},
+                    {kDim, row, row * rows}, box1, box2, who);
 }
 
 }  // namespace
@@ -187,9 +198,6 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   const size_t need = flint_tree_workspace_bytes(num_ctas);
   if (ws_bytes < need)
     return record_error(FLINT_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu needed", who, ws_bytes, need);
-  p.q = q;
-  p.k_draft = k_draft;
-  p.v_draft = v_draft;
   p.parent = parent;
   p.sinks = sinks;
   p.out = out;
@@ -213,6 +221,9 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   if (p.n_units == 0) return record_ok();
   s = tree_map(&p.k_map, c.k, c, B, who);
   if (s == FLINT_OK) s = tree_map(&p.v_map, c.v, c, B, who);
+  if (s == FLINT_OK) s = rows_map(&p.q_map, q, kHeads, B * N, kGroup, 8, who);
+  if (s == FLINT_OK) s = rows_map(&p.kd_map, k_draft, kKvHeads, B * N, 1, 64, who);
+  if (s == FLINT_OK) s = rows_map(&p.vd_map, v_draft, kKvHeads, B * N, 1, 64, who);
   if (s != FLINT_OK) return s;
   return launched(launch_tree(p, static_cast<cudaStream_t>(stream)), who);
 }

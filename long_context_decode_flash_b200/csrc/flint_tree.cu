@@ -15,27 +15,34 @@
 // read the same token rows at the same time; a unit cut between groups leaves
 // one partial per share (O, m, l), and a second launch folds them in order.
 //
-// A CTA is 14 warps over two streams of steps, a step being one row tile
+// A CTA is 15 working warps over two streams of steps, a step being one row tile
 // against one key tile.  Two row tiles: stream w is row tile w.  One row tile:
 // stream w is the key tiles of parity w, the two streams' states joined at the
 // item's end.  So either way one stream's softmax runs beside the other's MMAs:
-//   warp 12     TMA producer: 64-row boxes of K and V through one ring of
-//               32 KiB stages (128-byte swizzle).
-//   warps 8-11  make the stages MMA operands: V from bf16 to fp16 in place, or
-//               E4M3 codes (landed in the stage's upper half) of K and V to
-//               fp16; the drafted tokens' rows; Q; V rows that hold no token
-//               become 0 (whatever lies there must not meet a probability 0).
+//   warps 12, 14  TMA producers of K and V: 64-row boxes, the drafts' among them
+//               (128-byte swizzle).
+//   warps 8-11  make MMA operands of what is none: V to fp16 (bf16 in place, or
+//               E4M3 codes), the drafts through the cache's quantisation, Q against
+//               E4M3 to its two terms; V rows that hold no token become 0 (whatever
+//               lies there must not meet a probability 0).
 //   warp 13     issues S_w = Q K^T (M 128, N 128) and O_w += P_w V.
 //   warps 0-7   softmax, warpgroup w on stream w, a thread per row: fp32 online
 //               softmax in log2 units with a running maximum that moves only
-//               by more than 2^8; P goes back to TMEM over S's upper columns.
-// P is held in fp16 as 2^(x - m + 7): at most 2^15 under the lazy maximum, so
-// that probabilities keep 11 bits down to 2^-21 of the largest and lose at
-// most 2^-32 of it below (a bf16 P would round each by 2^-9).  V is fp16 (exact
-// for E4M3 and for bf16 in fp16's normal range, saturating at 65504).
-// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P_w
-// (fp16 pairs) is S_w's [64,128).  Every wait is bounded; a timeout raises
-// FLINT_ERR_TIMEOUT.
+//               by more than 2^8; P goes back to TMEM over S.
+// A unit of at most 8 nodes that is cut has its rows twice in the row tile, copy c
+// taking the c-th half of each key tile's keys with the other probabilities 0:
+// the MMAs cost the same, the softmax half.  The copies are partials of their
+// own, joined by the second launch.
+// P is one fp16 term, 2^(x - m + 7): at most 2^15 under the lazy maximum, so that
+// probabilities keep 11 bits down to 2^-21 of the largest and lose at most 2^-32
+// of it below (a bf16 P would round each by 2^-9; two bf16 terms made the softmax
+// and the PV product half as long again).  V is fp16 for it: exact for E4M3 and
+// for bf16 in fp16's normal range, saturating at 65504.  Against E4M3, K is the
+// codes themselves and q two E4M3 terms a value (split_q_rows), at twice the MMA
+// rate of 16-bit operands.
+// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).  P_w's fp16
+// pairs lie over S_w: those of keys 32 k .. 32 k + 31 at columns 32 k ..  32 k + 15.
+// Every wait is bounded; a timeout raises FLINT_ERR_TIMEOUT.
 #include <math.h>
 
 #include <algorithm>
@@ -52,50 +59,70 @@ constexpr int kTrNodes = kTrRows / kGroup;
 constexpr int kHalf = 64;                  // keys of a half tile
 constexpr int kTrKeys = 2 * kHalf;         // keys of a tile
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kConvThreads = kConvWarps * 32;
-constexpr int kTmaWarp = kSoftWarps + kConvWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kTrThreads = (kMmaWarp + 1) * 32;
+constexpr int kTmaWarp = kSoftWarps + kConvWarps, kMmaWarp = kTmaWarp + 1, kTmaWarpV = kTmaWarp + 2;
+constexpr int kTrThreads = 16 * 32;        // (one warp idle: registers are dealt out by warpgroups)
+// Registers a thread: launched with 128, then 256 softmax threads at 192 (a
+// row's 128 scores stay in registers), 128 converters and 128 others at 64.
+constexpr int kRegSoft = 192, kRegConv = 64, kRegRest = 64;
+static_assert(kTrThreads * 128 == 256 * kRegSoft + 128 * kRegConv + 128 * kRegRest, "the launch's registers");
 constexpr uint32_t kBox16 = kHalf * 128;            // 64 keys x 64 dims x 16 bit (or 128 dims x 8 bit): 8 KiB
 constexpr uint32_t kDimHalf = kTrKeys * 128;        // 64 dims of a 16-bit tile: 16 KiB
 constexpr uint32_t kStage = 2 * kDimHalf;           // a K or V tile: 32 KiB
+constexpr uint32_t kCodes = 2 * kBox16;             // 128 keys of codes, or 64 drafted rows in bf16: 16 KiB
 constexpr uint32_t kQTile = 2 * kTrRows * 128;      // a Q row tile: 32 KiB
 constexpr float kTrLog2e = 1.4426950408889634f;
 constexpr float kTrScale = static_cast<float>(1.4426950408889634 * 0.08838834764831845);
-constexpr float kTau = 8.0f;               // the running maximum lags by at most this (log2 units)
 constexpr float kBias = 7.0f;              // P = 2^(x - m + kBias)
-constexpr uint32_t kColS = 0, kColP = 64, kColO = 256;  // + 128 * stream
-constexpr int kInfo = 8;                   // tiles whose NaN record is kept
+constexpr float kTau = 8.0f;               // the running maximum lags by at most this (log2 units)
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
+constexpr int kInfo = 4;                   // tiles whose record of non-finite v is kept
 
-// MT row tiles a unit (1 or 2): the ring gets what Q leaves.
-template <int MT>
+// Shared memory for MT row tiles a unit (1 or 2): Q; a ring of K and V tiles in
+// bf16, or with an E4M3 cache rings of K codes (operands as they land), of V's
+// codes and of V's fp16 tiles.
+template <int MT, bool FP8>
 struct Lay {
-  static constexpr int kStages = MT == 1 ? 6 : 5;
-  static constexpr uint32_t kRing = MT * kQTile;
-  static constexpr uint32_t kEx = kRing + kStages * kStage;        // m, l of the two streams: [2 streams][128] float2
-  static constexpr uint32_t kNan = kEx + 2 * kTrRows * 8;          // [kInfo][4] words
-  static constexpr uint32_t kBar = kNan + kInfo * 16;
-  static constexpr size_t kBytes = kBar + 256;
+  static constexpr int kTiles = FP8 ? (MT == 1 ? 4 : 3) : (MT == 1 ? 6 : 5);  // bf16 K and V, or K codes
+  static constexpr uint32_t kTileBytes = FP8 ? kCodes : kStage;
+  static constexpr int kRaws = MT == 1 ? 4 : 3;                               // E4M3: V's codes, the drafts
+  static constexpr int kVs = 2;                                               // E4M3: V in fp16
+  static constexpr uint32_t kTile = MT * kQTile;
+  static constexpr uint32_t kRaw = kTile + kTiles * kTileBytes;
+  static constexpr uint32_t kV = kRaw + (FP8 ? kRaws * kCodes : 0);
+  static constexpr uint32_t kEx = kV + (FP8 ? kVs * kStage : 0);   // m, l of the two streams: [2 streams][128] float2
+  static constexpr uint32_t kNan = kEx + 2 * kTrRows * 8;          // [kInfo][8] words
+  static constexpr uint32_t kQExp = kNan + kInfo * 32;             // E4M3: exponents of Q's rows, int8 [2][128]
+  static constexpr uint32_t kBar = kQExp + 2 * kTrRows;
+  static constexpr size_t kBytes = kBar + 384;
 };
-static_assert(Lay<1>::kBytes <= 232448 && Lay<2>::kBytes <= 232448, "shared memory of a CTA");
+static_assert(Lay<1, false>::kBytes <= 232448 && Lay<2, false>::kBytes <= 232448 && Lay<1, true>::kBytes <= 232448 &&
+              Lay<2, true>::kBytes <= 232448, "shared memory of a CTA");
 
 struct Bars {
-  uint64_t full[6], ready[6], empty[6];  // stage landed / is an operand / was consumed
+  uint64_t full[6], empty[6];            // a tile (E4M3: K tile) landed; was consumed
+  uint64_t raw_full[4], raw_free[4];     // E4M3: V's codes, or drafts, landed; were read
+  uint64_t v_empty[2];                   // E4M3: an fp16 V tile was consumed
+  uint64_t v_ready[4];                   // V of tile T (mod 4) is an operand
+  uint64_t kd_ready;                     // E4M3, per item that begins its unit: the drafts' K codes written
   uint64_t s_full[2];                    // S_w complete (and every MMA issued before it)
   uint64_t p_ready[2];                   // P_w written, S_w read
-  uint64_t q_ready, q_empty;             // per item: Q filled; every S of the item complete
+  uint64_t q_full, q_empty;              // per item: Q landed; every S of the item complete
+  uint64_t q_ready, q_known;             // E4M3, per item: Q in two terms; its exponents read
   uint64_t o_full, o_free;               // per item: O complete; O read
   uint64_t ex_full;                      // per item with one row tile: m, l of both streams written
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
+  int q_armed;                           // items whose Q loads were issued
+  int armed[6], raw_armed[4];            // per stage: 1 + the last tile armed, 0 for none
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 384, "barrier block");
 
-// Instruction descriptors (kind::f16), fp32 D, M 128, N 128, A K-major.  S: B
-// (K) K-major, both bf16 or both fp16; PV: fp16, B (V) dims-major.
+// Instruction descriptors, fp32 D, M 128, N 128, A K-major; both operands bf16 or
+// both fp16 (kind::f16), or both E4M3 (kind::f8f6f4).  S: B (K) K-major; PV: B (V) dims-major.
 constexpr uint32_t kIdescBase = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescSBf16 = kIdescBase | (1u << 7) | (1u << 10);
-constexpr uint32_t kIdescSF16 = kIdescBase;
+constexpr uint32_t kIdescSE4m3 = kIdescBase;  // (kind::f8f6f4)
 constexpr uint32_t kIdescPV = kIdescBase | (1u << 16);
 
 // Shared-memory matrix descriptor, 128-byte swizzle.
@@ -107,6 +134,13 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ss8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -145,6 +179,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       FLINT_W8(0), FLINT_W8(8), FLINT_W8(16), FLINT_W8(24)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      FLINT_W8(0), FLINT_W8(8)
+      : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -157,39 +197,24 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Two floats -> packed f16x2 (first in the low half), nearest even, saturating
-// at +-65504; NaN stays NaN.
-__device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// acc + 0 * x per half: a half of acc turns NaN where x is.
-__device__ __forceinline__ uint32_t nan_acc(uint32_t acc, uint32_t x) {
-  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
-  return acc;
-}
-__device__ __forceinline__ uint32_t nan_to_zero(uint32_t x) {
-  if ((x & 0x7FFFu) > 0x7C00u) x &= 0xFFFF0000u;
-  if ((x & 0x7FFF0000u) > 0x7C000000u) x &= 0xFFFFu;
+// fp16 pairs with what is not finite made 0.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
+  if ((x & 0x7C00u) == 0x7C00u) x &= 0xFFFF0000u;
+  if ((x & 0x7C000000u) == 0x7C000000u) x &= 0xFFFFu;
   return x;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// True on every converter thread if `ok` is true on all of them.
-__device__ __forceinline__ bool conv_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.aligned.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok)), "n"(kConvThreads)
-      : "memory");
-  return r != 0;
-}
-
+// A bounded wait of a whole warp: true only if every lane saw the phase
+// complete.  The limit is counted in SM cycles (two to a nanosecond at the
+// highest clock).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Bars* B) {
-  const bool ok = mbar_wait(bar, parity, &B->abort);
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    do ok = mbar_try_wait(bar, parity);
+    while (!ok && *reinterpret_cast<const volatile int*>(&B->abort) == 0 && clock64() - t0 <= static_cast<long long>(2 * kWaitLimitNs));
+  }
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool aborted(const Bars* B) {
@@ -203,10 +228,11 @@ __device__ __forceinline__ void raise_abort(const TreeParams& p, Bars* B) {
 // The items of a CTA's group: (unit, tiles [t0, t1)) in order.
 struct Item {
   int u, t0, t1, i;      // i: number of the item in the group's list
-  int T, n[2];           // tiles and steps per stream of the items before this one
+  int T, n0, n1;         // tiles and steps of stream 0, 1 of the items before this one
   int steps, mt;
-  int x;                 // items with one row tile before this one
+  int x, d;              // items with one row tile, items that begin their unit, before this one
   __device__ bool whole(const TreeParams& p) const { return t0 == 0 && t1 == p.unit[u].tiles; }
+  __device__ int done(int w) const { return w ? n1 : n0; }
   __device__ int stream_steps(int w) const { return mt == 2 ? t1 - t0 : (t1 - t0 - w + 1) / 2; }
 };
 __device__ __forceinline__ bool clip(const TreeParams& p, int q, Item& it) {
@@ -220,37 +246,66 @@ __device__ __forceinline__ bool clip(const TreeParams& p, int q, Item& it) {
 __device__ __forceinline__ bool first_item(const TreeParams& p, int q, Item& it) {
   it.u = p.cut[q].unit;
   it.t0 = p.cut[q].tile;
-  it.i = it.x = 0;
-  it.T = it.n[0] = it.n[1] = 0;
+  it.i = it.x = it.d = 0;
+  it.T = it.n0 = it.n1 = 0;
   return clip(p, q, it);
 }
 __device__ __forceinline__ bool next_item(const TreeParams& p, int q, Item& it) {
-  it.n[0] += it.stream_steps(0);
-  it.n[1] += it.stream_steps(1);
+  it.n0 += it.stream_steps(0);
+  it.n1 += it.stream_steps(1);
   it.T += it.t1 - it.t0;
   it.x += it.mt == 1;
+  it.d += it.t0 == 0;
   ++it.i;
   ++it.u;
   it.t0 = 0;
   return clip(p, q, it);
 }
 
-// The producer warp (lane 0 issues; 32 page numbers are fetched at a time, a
-// batch ahead).  c counts stages: tile T's K is 2T, its V 2T + 1.  Returns the
-// stages armed.
-template <int MT, bool FP8>
-__device__ int run_tma(const TreeParams& p, int q, int g, uint32_t base, Bars* B, int lane) {
-  constexpr int NS = Lay<MT>::kStages;
-  int c = 0;
+// The order of an item's 2 n operand tiles is that of their first use.  Two row
+// tiles: K0 V0 K1 V1 ..; one (S runs two key tiles ahead): K0 K1 V0 K2 V1 .. V.
+__device__ __forceinline__ int seq_of(bool v, int j, int n, int mt) {
+  if (mt == 2) return 2 * j + v;
+  return v ? (j == n - 1 ? 2 * n - 1 : 2 * j + 2) : (j == 0 ? 0 : 2 * j - 1);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\t.reg .b32 r;\n\telect.sync r|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Waits for stage `c` of a ring of `size` and arms it with `bytes` (the elected
+// lane of a converged warp).
+__device__ __forceinline__ bool arm(int c, int size, uint64_t* gone, uint64_t* full, int* armed, uint32_t bytes, Bars* B) {
+  if (c >= size && !warp_wait(smem_u32(&gone[c % size]), static_cast<uint32_t>(c / size - 1) & 1u, B)) return false;
+  if (elect()) {
+    armed[c % size] = c + 1;
+    mbar_expect_tx(smem_u32(&full[c % size]), bytes);
+  }
+  return true;
+}
+
+// A producer warp: K's (kV false) or V's tiles of the items, in order.  As the
+// MMA warp, it runs converged and elects the issuing lane (one warp for both
+// kinds took ~1,300 cycles a tile: the kernel's pace).  Page numbers are fetched 32
+// at a time, a batch ahead.  False if a wait ran out.
+template <int MT, bool FP8, bool kV>
+__device__ __forceinline__ bool run_tma(const TreeParams& p, int q, int g, uint32_t base, Bars* B, int lane) {
+  using Y = Lay<MT, FP8>;
+  const CUtensorMap* map = kV ? &p.v_map : &p.k_map;
+  const CUtensorMap* draft = kV ? &p.vd_map : &p.kd_map;
+  int raws = 0;  // raw stages armed
   Item it;
   for (bool more = first_item(p, q, it); more; more = next_item(p, q, it)) {
     const TreeUnit& un = p.unit[it.u];
-    const int b = un.b;
+    const int b = un.b, n = it.t1 - it.t0;
     const bool paged = p.layout == FLINT_KV_PAGED;
     const int h0 = 2 * it.t0, h1 = min(2 * it.t1, un.halves);  // halves of the item; half h >= 1: box at base + 64 (h - 1)
-    auto page_of = [&](int h) {
+    auto pages = [&](int batch) {
+      const int h = h0 + 32 * batch + lane;
       int blk = 0;
-      if (h >= 1 && h < h1) {
+      if (paged && h >= 1 && h < h1) {
         blk = p.table[static_cast<long long>(b) * p.max_blocks + un.base / kBlock + h - 1];
         if (blk < 0 || blk >= p.num_blocks) {  // never handed to a load
           report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
@@ -259,272 +314,384 @@ __device__ int run_tma(const TreeParams& p, int q, int g, uint32_t base, Bars* B
       }
       return blk;
     };
-    int now = 0, ahead = paged ? page_of(h0 + lane) : 0;
-    for (int t = it.t0; t < it.t1; ++t) {
-      const int k = 2 * (t - it.t0);
-      if (paged && (k & 31) == 0) {
+    int now = 0, ahead = pages(0);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      if ((j & 15) == 0) {
         now = ahead;
-        ahead = page_of(h0 + k + 32 + lane);
+        ahead = pages((j >> 4) + 1);
       }
-      int row[2], req[2];
-      bool box[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 2 * t + e;
-        box[e] = h >= 1 && h < h1;
-        row[e] = paged ? 0 : un.base + (h - 1) * kHalf;
-        req[e] = paged ? __shfl_sync(0xffffffffu, now, (k & 31) + e) : b;
-      }
-      const uint32_t bytes = (box[0] ? 1u : 0u) + (box[1] ? 1u : 0u);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++c) {
-        const int st = c % NS;
-        if (c >= NS && !warp_wait(smem_u32(&B->empty[st]), static_cast<uint32_t>(c / NS - 1) & 1u, B)) {
-          if (lane == 0) raise_abort(p, B);
-          return c;
-        }
-        if (__any_sync(0xffffffffu, aborted(B))) return c;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&B->full[st]), dst = base + Lay<MT>::kRing + st * kStage;
-          const CUtensorMap* map = kv ? &p.v_map : &p.k_map;
-          mbar_expect_tx(bar, bytes * (FP8 ? kBox16 : 2 * kBox16));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (!box[e]) continue;
-            if (FP8) {
-              tma_load_4d(dst + kDimHalf + e * kBox16, map, bar, 0, g, row[e], req[e]);
-            } else {
-              tma_load_4d(dst + e * kBox16, map, bar, 0, g, row[e], req[e]);
-              tma_load_4d(dst + kDimHalf + e * kBox16, map, bar, 64, g, row[e], req[e]);
+      const int h = h0 + 2 * j;
+      const bool box0 = h >= 1, box1 = h + 1 < h1;  // (box 0 exists behind half 0: h < h1)
+      const int row0 = paged ? 0 : un.base + (h - 1) * kHalf, row1 = paged ? 0 : row0 + kHalf;
+      const int req0 = paged ? __shfl_sync(0xffffffffu, now, 2 * j & 31) : b;
+      const int req1 = paged ? __shfl_sync(0xffffffffu, now, (2 * j & 31) + 1) : b;
+      const uint32_t boxes = (box0 ? 1u : 0u) + (box1 ? 1u : 0u);
+      if (FP8) {
+        // K's codes to their ring, V's to theirs; the drafts (64 rows from the
+        // request's first node on) in bf16 to V's, K's by V's producer too
+        if (kV && h == 0) {
+#pragma unroll 1
+          for (int d = 0; d < 2; ++d) {
+            if (!arm(raws, Y::kRaws, B->raw_free, B->raw_full, B->raw_armed, 2 * kBox16, B)) return false;
+            const uint32_t bar = smem_u32(&B->raw_full[raws % Y::kRaws]), dst = base + Y::kRaw + (raws % Y::kRaws) * kCodes;
+            if (elect()) {
+              tma_load_4d(dst, d ? &p.vd_map : &p.kd_map, bar, 0, g, b * p.N, 0);
+              tma_load_4d(dst + kBox16, d ? &p.vd_map : &p.kd_map, bar, 64, g, b * p.N, 0);
             }
+            ++raws;
           }
         }
-        __syncwarp();
+        const int c = kV ? raws : it.T + j, size = kV ? Y::kRaws : Y::kTiles;
+        uint64_t* full = kV ? B->raw_full : B->full;
+        if (!arm(c, size, kV ? B->raw_free : B->empty, full, kV ? B->raw_armed : B->armed, boxes * kBox16, B)) return false;
+        const uint32_t bar = smem_u32(&full[c % size]), dst = base + (kV ? Y::kRaw : Y::kTile) + (c % size) * kCodes;
+        if (elect()) {
+          if (box0) tma_load_4d(dst, map, bar, 0, g, row0, req0);
+          if (box1) tma_load_4d(dst + kBox16, map, bar, 0, g, row1, req1);
+        }
+        if (kV) ++raws;
+      } else {
+        const int c = 2 * it.T + seq_of(kV, j, n, it.mt);
+        if (!arm(c, Y::kTiles, B->empty, B->full, B->armed, (boxes + (h == 0 ? 1u : 0u)) * 2 * kBox16, B)) return false;
+        const uint32_t bar = smem_u32(&B->full[c % Y::kTiles]), dst = base + Y::kTile + (c % Y::kTiles) * kStage;
+        if (elect()) {
+          if (box0) {
+            tma_load_4d(dst, map, bar, 0, g, row0, req0);
+            tma_load_4d(dst + kDimHalf, map, bar, 64, g, row0, req0);
+          }
+          if (box1) {
+            tma_load_4d(dst + kBox16, map, bar, 0, g, row1, req1);
+            tma_load_4d(dst + kDimHalf + kBox16, map, bar, 64, g, row1, req1);
+          }
+          if (h == 0) {
+            tma_load_4d(dst, draft, bar, 0, g, b * p.N, 0);
+            tma_load_4d(dst + kDimHalf, draft, bar, 64, g, b * p.N, 0);
+          }
+        }
       }
     }
   }
-  return c;
+  return true;
 }
 
-// Chunk `c` (8 values of 16 bit, c in [0, 16)) of row r in a 128-byte-swizzled
-// operand tile of two 64-dim halves.
-__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
-  return tile + (c >> 3) * kDimHalf + r * 128 + ((c ^ r) & 7) * 16;
+// Byte offset of chunk `c` (8 values of 16 bit, c in [0, 16)) of row r in a
+// 128-byte-swizzled operand tile of two 64-dim halves.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (c >> 3) * kDimHalf + r * 128 + ((c ^ r) & 7) * 16;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ uint4& smem4(uint8_t* p) { return *reinterpret_cast<uint4*>(p); }
+// Two floats -> packed f16x2 (first in the low half), nearest even, saturating
+// at +-65504; NaN stays NaN.
+__device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 __device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v) {
   return make_uint4(f16x2_sat(bf16_lo(v.x), bf16_hi(v.x)), f16x2_sat(bf16_lo(v.y), bf16_hi(v.y)),
                     f16x2_sat(bf16_lo(v.z), bf16_hi(v.z)), f16x2_sat(bf16_lo(v.w), bf16_hi(v.w)));
 }
-// bf16 values as an E4M3 cache of this scale holds them, in units of the scale.
-__device__ __forceinline__ uint32_t bf16x2_through_e4m3(uint32_t w, float scale) {
-  const uint32_t code = f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(w), scale), __fdiv_rn(bf16_hi(w), scale));
-  uint32_t lo, hi;
-  e4m3x4_to_f16x2x2(code, lo, hi);
-  return lo;
+// The codes that an E4M3 cache of this scale holds for two bf16 values.
+__device__ __forceinline__ uint32_t bf16x2_to_e4m3(uint32_t w, float scale) {
+  return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(w), scale), __fdiv_rn(bf16_hi(w), scale));
 }
 
-// The converter warps (thread ct of 128).  Every barrier of theirs is reached
-// by all four warps, whatever their waits returned.
+// What is not finite in a 16-byte chunk made 0; true if there was any.
+__device__ __forceinline__ bool make_finite(uint4& v) {
+  const uint4 f = make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+  const bool any = f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
+  v = f;
+  return any;
+}
+
+// A warp's 32 rows of a Q tile, bf16, into two E4M3 terms in place: with 2^e the
+// power of two that brings a row's largest magnitude into [128, 256), q 2^e = t1
+// + t2 up to 2^-10 (exact for magnitudes down to 2^-9 of the largest: bf16 has 8
+// bits, each term 4).  t1's 128 codes take the first 64-dim half's row, t2's the
+// second's.  Two rows at a time, 16 lanes each.  exps gets e; a row with
+// something not finite becomes NaN.
+__device__ __forceinline__ void split_q_rows(uint8_t* tile, int row0, int8_t* exps, int lane) {
+  const int c = lane & 15;
+#pragma unroll 2
+  for (int i = 0; i < 16; ++i) {
+    const int r = row0 + 2 * i + (lane >> 4);
+    const uint4 y = smem4(tile + chunk_at(r, c));
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max3_nan(top, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max3_nan(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
+    const int field = static_cast<int>(__float_as_uint(top) >> 23 & 255u);  // biased exponent
+    const int e = field == 0 ? 0 : min(126, 134 - field);                 // (a row of 0 or subnormal: any)
+    const float up = field == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    uint32_t t1[2], t2[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float a = bf16_lo(w[2 * k]) * up, b = bf16_hi(w[2 * k]) * up;
+      const float u = bf16_lo(w[2 * k + 1]) * up, v = bf16_hi(w[2 * k + 1]) * up;
+      t1[k] = f32x2_to_e4m3x2(a, b) | f32x2_to_e4m3x2(u, v) << 16;
+      uint32_t lo, hi;
+      e4m3x4_to_f16x2x2(t1[k], lo, hi);
+      const float2 ab = __half22float2(*reinterpret_cast<__half2*>(&lo)), uv = __half22float2(*reinterpret_cast<__half2*>(&hi));
+      t2[k] = f32x2_to_e4m3x2(a - ab.x, b - ab.y) | f32x2_to_e4m3x2(u - uv.x, v - uv.y) << 16;
+    }
+    __syncwarp();  // both rows are read
+    uint8_t* at = tile + chunk_at(r, c >> 1) + (c & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(t1[0], t1[1]);
+    *reinterpret_cast<uint2*>(at + kDimHalf) = make_uint2(t2[0], t2[1]);
+    if (c == 0) exps[r] = static_cast<int8_t>(e);
+  }
+}
+
+// The converter warps (thread ct of 128, which owns row ct of a tile).  False
+// if a wait ran out.
 template <int MT, bool FP8>
-__device__ void run_conv(const TreeParams& p, int q, int g, uint32_t base, uint8_t* smem, Bars* B, int ct) {
-  constexpr int NS = Lay<MT>::kStages;
+__device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint8_t* smem, Bars* B, int ct) {
+  using Y = Lay<MT, FP8>;
   const int lane = ct & 31, warp = ct >> 5;
-  uint32_t* nans = reinterpret_cast<uint32_t*>(smem + Lay<MT>::kNan);
+  int raw = 0;  // E4M3: stages of codes and drafts read so far
+  auto raw_stage = [&] { return smem + Y::kRaw + (raw % Y::kRaws) * kCodes; };
+  auto raw_wait = [&] { return warp_wait(smem_u32(&B->raw_full[raw % Y::kRaws]), static_cast<uint32_t>(raw / Y::kRaws) & 1u, B); };
+  auto raw_done = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&B->raw_free[raw % Y::kRaws]));
+    ++raw;
+  };
   Item it;
   for (bool more = first_item(p, q, it); more; more = next_item(p, q, it)) {
     const TreeUnit& un = p.unit[it.u];
-    const int b = un.b, n = p.n_draft[b];
-    const long long node0 = static_cast<long long>(b) * p.N;
-    // Q: row r of tile m is head g * 8 + (r & 7) of node 32 rb + 16 m + (r >> 3)
-    bool ok = it.i == 0 || warp_wait(smem_u32(&B->q_empty), static_cast<uint32_t>(it.i - 1) & 1u, B);
-    if (!conv_all(ok)) {
-      if (ct == 0) raise_abort(p, B);
-      return;
+    const int b = un.b, nd = p.n_draft[b], n = it.t1 - it.t0;
+    const uint32_t before = static_cast<uint32_t>(it.i - 1) & 1u;
+    if (warp == 0) {
+      if (it.i > 0 && !warp_wait(smem_u32(&B->q_empty), before, B)) return false;
+      if (lane == 0) {
+        // Q: row r of tile m is head g * 8 + (r & 7) of node 32 rb + 16 m + (r >> 3);
+        // boxes of 8 nodes, the first one again for a second copy of the rows
+        // (rows behind the request's nodes are anything: no row meets another)
+        const uint32_t bar = smem_u32(&B->q_full), dst = smem_u32(smem);
+        B->q_armed = it.i + 1;
+        mbar_expect_tx(bar, it.mt * kQTile);
+#pragma unroll 1
+        for (int x = 0; x < 4 * it.mt; ++x) {
+          const int m = x >> 2, half = x >> 1 & 1, dims = x & 1;
+          const int node = b * p.N + un.rb * 2 * kTrNodes + m * kTrNodes + (un.dup == 1 ? half * 8 : 0);
+          tma_load_4d(dst + m * kQTile + dims * kDimHalf + half * kBox16, &p.q_map, bar, 64 * dims, g * kGroup, node, 0);
+        }
+      }
+      __syncwarp();
     }
-#pragma unroll 4
-    for (int i = 0; i < it.mt * (kTrRows * 16 / kConvThreads); ++i) {
-      const int x = i * kConvThreads + ct, c = x & 15, r = x >> 4;
-      const int node = un.rb * 2 * kTrNodes + (r >> 3);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (node < n) v = reinterpret_cast<const uint4*>(p.q + ((node0 + node) * kHeads + g * kGroup + (r & 7)) * kDim)[c];
-      if (FP8) v = bf16x8_to_f16(v);
-      sts128(chunk_at(base + (r >> 7) * kQTile, r & 127, c), v);
+    if (FP8) {
+      const int j = ct & 63;
+      if (it.t0 == 0) {  // the drafts' K as the cache would hold it: codes, half a row a thread
+        const int c = it.T;  // (the item's first K tile)
+        if (!raw_wait() || !warp_wait(smem_u32(&B->full[c % Y::kTiles]), static_cast<uint32_t>(c / Y::kTiles) & 1u, B)) return false;
+        const uint8_t* from = raw_stage() + (ct >> 6) * kBox16 + j * 128;
+        uint8_t* to = smem + Y::kTile + (c % Y::kTiles) * kCodes + j * 128;
+        const float scale = p.k_scale[g];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // 16 values, one chunk of codes
+          uint32_t code[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 y = *reinterpret_cast<const uint4*>(from + (((2 * i + k) ^ j) & 7) * 16);
+            code[2 * k] = bf16x2_to_e4m3(y.x, scale) | bf16x2_to_e4m3(y.y, scale) << 16;
+            code[2 * k + 1] = bf16x2_to_e4m3(y.z, scale) | bf16x2_to_e4m3(y.w, scale) << 16;
+          }
+          smem4(to + (((4 * (ct >> 6) + i) ^ j) & 7) * 16) = make_uint4(code[0], code[1], code[2], code[3]);
+        }
+        fence_async_smem();
+        raw_done();
+        if (lane == 0) mbar_arrive(smem_u32(&B->kd_ready));
+      }
+      if (it.i > 0 && !warp_wait(smem_u32(&B->q_known), before, B)) return false;
+      if (!warp_wait(smem_u32(&B->q_full), static_cast<uint32_t>(it.i) & 1u, B)) return false;
+#pragma unroll 1
+      for (int m = 0; m < it.mt; ++m)
+        split_q_rows(smem + m * kQTile, 32 * warp, reinterpret_cast<int8_t*>(smem + Y::kQExp) + m * kTrRows, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B->q_ready));
     }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&B->q_ready));
-
-    for (int t = it.t0; t < it.t1; ++t) {
-      const int T = it.T + t - it.t0;
-      // row ct of the tile: does a token stand there?  (V; half 0 is the drafts')
+#pragma unroll 1
+    for (int tj = 0; tj < n; ++tj) {  // V
+      const int t = it.t0 + tj, T = it.T + tj;
+      uint32_t* lost = reinterpret_cast<uint32_t*>(smem + Y::kNan) + (T % kInfo) * 8;
+      // does a token stand in row ct of the tile (half 0 is the drafts'), and may
+      // some node not attend it?
       const int h = 2 * t + (ct >> 6), j = ct & 63;
-      bool token;
+      bool token, scan;
       if (h == 0) {
-        token = j < n;
+        token = scan = j < nd;
       } else {
         const int s = un.base + (h - 1) * kHalf + j;
         token = h < un.halves && s >= un.lo && s < un.hi;
+        scan = token && p.window > 0 && (p.layout == FLINT_KV_RING || s < un.lo + kMaxTree);
       }
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int c = 2 * T + kv, st = c % NS;
-        const uint32_t tile = base + Lay<MT>::kRing + st * kStage;
-        ok = warp_wait(smem_u32(&B->full[st]), static_cast<uint32_t>(c / NS) & 1u, B);
-        uint4 code[8];
-        if (FP8) {
-          // (rows of an absent box hold old bytes; they are zeroed or masked)
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) code[k] = lds128(tile + kDimHalf + ct * 128 + ((k ^ ct) & 7) * 16);
+      uint8_t* tile;
+      uint32_t half_rows = 0;  // record of the drafts' rows' second halves
+      bool has = false;  // something in the row was not finite
+      if (FP8) {
+        tile = smem + Y::kV + (T % Y::kVs) * kStage;
+        if (T >= Y::kVs && !warp_wait(smem_u32(&B->v_empty[T % Y::kVs]), static_cast<uint32_t>(T / Y::kVs - 1) & 1u, B)) return false;
+        if (t == 0) {  // the drafts, half a row a thread
+          if (!raw_wait()) return false;
+          const uint8_t* from = raw_stage() + (ct >> 6) * kBox16 + j * 128;
+          const float scale = p.v_scale[g];
+          bool bad = false;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4*>(from + ((i ^ j) & 7) * 16);
+            uint4 z = make_uint4(0, 0, 0, 0);
+            if (j < nd) {
+              const uint32_t a = bf16x2_to_e4m3(y.x, scale) | bf16x2_to_e4m3(y.y, scale) << 16;
+              const uint32_t d = bf16x2_to_e4m3(y.z, scale) | bf16x2_to_e4m3(y.w, scale) << 16;
+              e4m3x4_to_f16x2x2(a, z.x, z.y);
+              e4m3x4_to_f16x2x2(d, z.z, z.w);
+            }
+            bad |= make_finite(z);
+            smem4(tile + chunk_at(j, 8 * (ct >> 6) + i)) = z;
           }
+          half_rows = __ballot_sync(0xffffffffu, bad);
+          raw_done();
         }
-        if (!conv_all(ok)) {
-          if (ct == 0) raise_abort(p, B);
-          return;
-        }
-        uint32_t bad = 0;  // NaN in this row?
-        if (FP8 && h > 0) {
+        if (!raw_wait()) return false;
+        uint4 code[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) code[k] = smem4(raw_stage() + ct * 128 + ((k ^ ct) & 7) * 16);
+        raw_done();
+        if (h > 0) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            uint4 a = make_uint4(0, 0, 0, 0), d = a;
-            if (kv == 0 || token) {
-              e4m3x4_to_f16x2x2(code[k].x, a.x, a.y);
-              e4m3x4_to_f16x2x2(code[k].y, a.z, a.w);
-              e4m3x4_to_f16x2x2(code[k].z, d.x, d.y);
-              e4m3x4_to_f16x2x2(code[k].w, d.z, d.w);
-            }
-            if (kv) {
-              bad = nan_acc(nan_acc(nan_acc(nan_acc(bad, a.x), a.y), a.z), a.w);
-              bad = nan_acc(nan_acc(nan_acc(nan_acc(bad, d.x), d.y), d.z), d.w);
-            }
-            sts128(chunk_at(tile, ct, 2 * k), a);
-            sts128(chunk_at(tile, ct, 2 * k + 1), d);
+            if (!token) code[k] = make_uint4(0, 0, 0, 0);
+            uint4 a, d;
+            e4m3x4_to_f16x2x2(code[k].x, a.x, a.y);
+            e4m3x4_to_f16x2x2(code[k].y, a.z, a.w);
+            e4m3x4_to_f16x2x2(code[k].z, d.x, d.y);
+            e4m3x4_to_f16x2x2(code[k].w, d.z, d.w);
+            smem4(tile + chunk_at(ct, 2 * k)) = a;
+            smem4(tile + chunk_at(ct, 2 * k + 1)) = d;
           }
         }
-        if (!FP8 && kv == 1 && h > 0) {
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t at = chunk_at(tile, ct, k);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (token) v = bf16x8_to_f16(lds128(at));
-            bad = nan_acc(nan_acc(nan_acc(nan_acc(bad, v.x), v.y), v.z), v.w);
-            sts128(at, v);
-          }
+      } else {
+        const int c = 2 * it.T + seq_of(true, tj, n, it.mt);
+        tile = smem + Y::kTile + (c % Y::kTiles) * kStage;
+        if (!warp_wait(smem_u32(&B->full[c % Y::kTiles]), static_cast<uint32_t>(c / Y::kTiles) & 1u, B)) return false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint4 y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = smem4(tile + chunk_at(ct, 8 * x + k));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) smem4(tile + chunk_at(ct, 8 * x + k)) = token ? bf16x8_to_f16(y[k]) : make_uint4(0, 0, 0, 0);
         }
-        if (t == 0) {  // the drafts: rows 0..63, 16 lanes a row
-          const uint16_t* src = kv ? p.v_draft : p.k_draft;
-          const float scale = FP8 ? (kv ? p.v_scale[g] : p.k_scale[g]) : 1.f;
-#pragma unroll 2
-          for (int i = 0; i < kHalf * 16 / kConvThreads; ++i) {
-            const int x = i * kConvThreads + ct, cc = x & 15, r = x >> 4;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < n) v = reinterpret_cast<const uint4*>(src + ((node0 + r) * kKvHeads + g) * kDim)[cc];
-            if (FP8) {
-              v = make_uint4(bf16x2_through_e4m3(v.x, scale), bf16x2_through_e4m3(v.y, scale),
-                             bf16x2_through_e4m3(v.z, scale), bf16x2_through_e4m3(v.w, scale));
-            } else if (kv) {
-              v = bf16x8_to_f16(v);
-            }
-            sts128(chunk_at(tile, r, cc), v);
-          }
-          if (kv) {  // their NaN record wants whole rows
-            if (!conv_all(true)) return;
-            if (h == 0) {
-#pragma unroll 4
-              for (int k = 0; k < 16; ++k) {
-                const uint4 v = lds128(chunk_at(tile, ct, k));
-                bad = nan_acc(nan_acc(nan_acc(nan_acc(bad, v.x), v.y), v.z), v.w);
-              }
-            }
-          }
-        }
-        if (kv) {
-          const bool has = nan_to_zero(bad) != bad;
-          if (has) {  // 0 in its place, for rows that do not attend the key; the others learn of it by the record
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const uint32_t at = chunk_at(tile, ct, k);
-              const uint4 v = lds128(at);
-              sts128(at, make_uint4(nan_to_zero(v.x), nan_to_zero(v.y), nan_to_zero(v.z), nan_to_zero(v.w)));
-            }
-          }
-          const uint32_t word = __ballot_sync(0xffffffffu, has);
-          if (lane == 0) nans[(T % kInfo) * 4 + warp] = word;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&B->ready[st]));
       }
+      if (scan && !(FP8 && h == 0)) {
+        // What is not finite becomes 0, for the rows that do not attend the
+        // key; the rows that do learn of it by the record.
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+          uint4 y = smem4(tile + chunk_at(ct, k));
+          if (make_finite(y)) {
+            has = true;
+            smem4(tile + chunk_at(ct, k)) = y;
+          }
+        }
+      }
+      const uint32_t word = __ballot_sync(0xffffffffu, has);
+      if (lane == 0) {
+        // words 0..3: the rows; 4, 5: the drafts' rows, their second halves
+        lost[warp] = FP8 && t == 0 && warp < 2 ? half_rows : word;
+        if (warp >= 2) lost[2 + warp] = half_rows;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B->v_ready[T & 3]));
     }
   }
-}
-
-// S of the item's step s (row tile and key tile by the mode): 8 MMAs of 16 dims.
-template <int MT, bool FP8>
-__device__ __forceinline__ bool issue_s(const Item& it, int s, uint32_t base, uint32_t tmem, Bars* B) {
-  constexpr int NS = Lay<MT>::kStages;
-  const int w = s & 1, two = it.mt == 2;
-  const int T = it.T + (two ? s >> 1 : s), c = 2 * T, st = c % NS;
-  const uint32_t parity = static_cast<uint32_t>(c / NS) & 1u;
-  if (!mbar_wait(smem_u32(&B->ready[st]), parity, &B->abort) || !mbar_wait(smem_u32(&B->full[st]), parity, &B->abort))
-    return false;
-  tc_fence_after();
-  const uint32_t qa = base + (two ? w * kQTile : 0), kb = base + Lay<MT>::kRing + st * kStage;
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = (kk >> 2) * kDimHalf + (kk & 3) * 32;
-    umma_ss(tmem + kColS + 128 * w, sw128_desc(qa + off, 16, 1024), sw128_desc(kb + off, 16, 1024),
-            FP8 ? kIdescSF16 : kIdescSBf16, kk > 0 ? 1u : 0u);
-  }
-  if (!two || w) umma_commit(smem_u32(&B->empty[st]));
-  umma_commit(smem_u32(&B->s_full[w]));
-  if (s == it.steps - 1) umma_commit(smem_u32(&B->q_empty));
   return true;
 }
 
-// The MMA thread: per item S of the first two steps, then per step PV and the
-// S two steps ahead (same stream: it overwrites P, whose PV is issued before).
+// The MMA warp, over its items' steps: S of the first two, then per step PV and
+// the S two steps ahead (of the same stream: it overwrites P, whose PV is issued
+// before).  The warp runs converged and elects the issuing lane around the MMAs,
+// on operands that are the same for the whole warp: then the compiler keeps them
+// in uniform registers and an M128 N128 K16 MMA issues every 64 cycles, the
+// tensor core's own rate.  (Issued by `if (lane == 0)` code, it measured 143.)
+// A barrier's test takes ~130 cycles, so a step's are issued together.
 template <int MT, bool FP8>
-__device__ void run_mma(const TreeParams& p, int q, uint32_t base, uint32_t tmem, Bars* B) {
-  constexpr int NS = Lay<MT>::kStages;
+__device__ __forceinline__ void run_mma(const TreeParams& p, int q, uint32_t base, uint32_t tmem, Bars* B, int lane) {
+  using Y = Lay<MT, FP8>;
   bool ok = true;
   Item it;
   for (bool more = first_item(p, q, it); ok && more; more = next_item(p, q, it)) {
-    ok = mbar_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, &B->abort);
-    if (ok) ok = issue_s<MT, FP8>(it, 0, base, tmem, B);
-    if (ok && it.steps > 1) ok = issue_s<MT, FP8>(it, 1, base, tmem, B);
-    // O of the item before must have been read
-    if (ok && it.i > 0) ok = mbar_wait(smem_u32(&B->o_free), static_cast<uint32_t>(it.i - 1) & 1u, &B->abort);
-    for (int s = 0; ok && s < it.steps; ++s) {
-      const int w = s & 1, two = it.mt == 2;
-      const int T = it.T + (two ? s >> 1 : s), c = 2 * T + 1, st = c % NS;
-      const uint32_t parity = static_cast<uint32_t>(c / NS) & 1u;
-      ok = mbar_wait(smem_u32(&B->p_ready[w]), static_cast<uint32_t>(it.n[w] + (s >> 1)) & 1u, &B->abort) &&
-           mbar_wait(smem_u32(&B->ready[st]), parity, &B->abort) && mbar_wait(smem_u32(&B->full[st]), parity, &B->abort);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t vb = base + Lay<MT>::kRing + st * kStage;
-      // O += P V: 16 keys per MMA (their fp16 pairs are 8 columns of P)
+    const int n = it.t1 - it.t0, two = it.mt == 2;
+    ok = warp_wait(smem_u32(FP8 ? &B->q_ready : &B->q_full), static_cast<uint32_t>(it.i) & 1u, B);
+    if (FP8 && ok && it.t0 == 0) ok = warp_wait(smem_u32(&B->kd_ready), static_cast<uint32_t>(it.d) & 1u, B);
+#pragma unroll 1
+    for (int s = -2; ok && s < it.steps; ++s) {
+      const int w = s & 1, s2 = s + 2;
+      // step s2's K tile
+      const bool more_s = s2 < it.steps;
+      const int tk = two ? s2 >> 1 : s2, ck = FP8 ? it.T + tk : 2 * it.T + seq_of(false, tk, n, it.mt), sk = ck % Y::kTiles;
+      const uint32_t k_bar = smem_u32(&B->full[sk]), k_par = static_cast<uint32_t>(ck / Y::kTiles) & 1u;
+      bool k_ok = !more_s || mbar_try_wait(k_bar, k_par);
+      if (s >= 0) {
+        const int tv = two ? s >> 1 : s, T = it.T + tv, cv = 2 * it.T + seq_of(true, tv, n, it.mt), sv = cv % Y::kTiles;
+        const uint32_t p_bar = smem_u32(&B->p_ready[w]), p_par = static_cast<uint32_t>(it.done(w) + (s >> 1)) & 1u;
+        const uint32_t v_bar = smem_u32(&B->v_ready[T & 3]), v_par = static_cast<uint32_t>(T >> 2) & 1u;
+        const bool p_ok = mbar_try_wait(p_bar, p_par), v_ok = mbar_try_wait(v_bar, v_par);
+        if (!__all_sync(0xffffffffu, p_ok && v_ok)) {
+          ok = warp_wait(p_bar, p_par, B) && warp_wait(v_bar, v_par, B);
+          if (!ok) break;
+        }
+        // O of the item before must have been read
+        if (s == 0 && it.i > 0 && !(ok = warp_wait(smem_u32(&B->o_free), static_cast<uint32_t>(it.i - 1) & 1u, B))) break;
+        tc_fence_after();
+        const uint64_t vd = sw128_desc(base + (FP8 ? Y::kV + (T % Y::kVs) * kStage : Y::kTile + sv * kStage), kDimHalf, 1024);
+        const uint32_t d = tmem + kColO + 128 * w, at = tmem + kColS + 128 * w, acc = s > 1 ? 1u : 0u;
+        if (elect()) {
+          // O += P V: 16 keys per MMA (their pairs are 8 columns of P)
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        umma_ts(tmem + kColO + 128 * w, tmem + kColP + 128 * w + kk * 8, sw128_desc(vb + kk * 16 * 128, kDimHalf, 1024),
-                kIdescPV, (s > 1 || kk > 0) ? 1u : 0u);
-      if (!two || w) umma_commit(smem_u32(&B->empty[st]));
-      if (s == it.steps - 1) umma_commit(smem_u32(&B->o_full));
-      if (s + 2 < it.steps) ok = issue_s<MT, FP8>(it, s + 2, base, tmem, B);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t v = vd + ((kk * 16 * 128) >> 4);
+            umma_ts(d, at + 32 * (kk >> 1) + 8 * (kk & 1), v, kIdescPV, kk > 0 ? 1u : acc);
+          }
+          if (!two || w) umma_commit(smem_u32(FP8 ? &B->v_empty[T % Y::kVs] : &B->empty[sv]));
+          if (s == it.steps - 1) umma_commit(smem_u32(&B->o_full));
+        }
+        __syncwarp();
+      }
+      if (more_s) {
+        if (!__all_sync(0xffffffffu, k_ok)) {
+          ok = warp_wait(k_bar, k_par, B);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        // S = Q K^T: 16 dims per MMA, or 32 in each of Q's two E4M3 terms
+        const uint64_t qd = sw128_desc(base + (two ? w * kQTile : 0), 16, 1024);
+        const uint64_t kd = sw128_desc(base + Y::kTile + sk * Y::kTileBytes, 16, 1024);
+        const uint32_t d = tmem + kColS + 128 * w;
+        if (elect()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * kDimHalf + (kk & 3) * 32) >> 4;
+            if (FP8) umma_ss8(d, qd + off, kd + (((kk & 3) * 32) >> 4), kIdescSE4m3, kk > 0 ? 1u : 0u);
+            else umma_ss(d, qd + off, kd + off, kIdescSBf16, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(smem_u32(&B->s_full[w]));
+          if (!two || w) umma_commit(smem_u32(&B->empty[sk]));
+          if (s2 == it.steps - 1) umma_commit(smem_u32(&B->q_empty));
+        }
+        __syncwarp();
+      }
     }
   }
-  if (!ok) raise_abort(p, B);
+  if (!ok && lane == 0) raise_abort(p, B);
   // let every issued MMA finish before the CTA ends (its TMEM is freed)
-  umma_commit(smem_u32(&B->mma_done));
+  if (elect()) umma_commit(smem_u32(&B->mma_done));
+  __syncwarp();
   const unsigned long long t0 = globaltimer_ns();
   while (!mbar_try_wait(smem_u32(&B->mma_done), 0))
     if (globaltimer_ns() - t0 > kWaitLimitNs) break;
@@ -598,19 +765,80 @@ __device__ __forceinline__ uint32_t mask_word(const TreeParams& p, const TreeUni
   return range_bits(s0, row.lo, row.hi);
 }
 
+// One step of a row: S to P (P's pairs lie over their own 32-key chunk of S),
+// and O brought to the new maximum where it moved.  The row's scores stay in
+// registers (one TMEM wait).  Chunks outside `mine` (a bit a chunk) belong to
+// the row's other copy and get probability 0.
+__device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float scale, uint32_t mine, bool first, float& m, float& l) {
+  uint32_t v[4][32];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tmem_ld32(sp + 32 * k, v[k]);
+  tmem_wait_ld();
+  float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 4; k += 2)
+    if (mine >> k & 1u) {
+#pragma unroll
+      for (int i = 0; i < 64; i += 2)
+        mq[(i >> 1) & 3] = max3_nan(mq[(i >> 1) & 3], __uint_as_float(v[k + (i >> 5)][i & 31]), __uint_as_float(v[k + (i >> 5)][(i & 31) + 1]));
+    }
+  const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]) * scale - kBias;
+  float factor = 1.f;
+  const bool need = !(mx <= m + kTau) && mx != -INFINITY;  // (NaN needs)
+  if (need) {
+    factor = m == -INFINITY ? 0.f : ex2(m - mx);
+    m = mx;
+    l *= factor;
+  }
+  const float2 scale2 = make_float2(scale, scale), nmu = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+  float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t pk[16];
+    if (mine >> k & 1u) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 x = fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), scale2, nmu);
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        ls[c & 1] = add2(ls[c & 1], e);
+        const __half2 hp = __floats2half2_rn(e.x, e.y);
+        pk[c] = *reinterpret_cast<const uint32_t*>(&hp);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) pk[c] = 0u;
+    }
+    tmem_st16(sp + 32 * k, pk);
+  }
+  const float2 lsum = add2(ls[0], ls[1]);
+  l += lsum.x + lsum.y;
+  if (!first && __any_sync(0xffffffffu, need)) {
+    // O_w holds the stream's earlier steps: their PV completed before this S
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      tmem_ld32(op + 32 * c, v[0]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * factor);
+      tmem_st32(op + 32 * c, v[0]);
+    }
+  }
+  tmem_wait_st();
+}
+
 // Softmax of one item by warpgroup w.  False if a wait ran out.
-template <int MT>
-__device__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, float scale, uint32_t tmem, uint8_t* smem,
-                             Bars* B, int warp, int lane) {
-  constexpr int NS = Lay<MT>::kStages;
+template <int MT, bool FP8>
+__device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, float scale, uint32_t tmem,
+                                             uint8_t* smem, Bars* B, int warp, int lane) {
+  using Y = Lay<MT, FP8>;
   const TreeUnit& un = p.unit[it.u];
-  const int w = warp >> 2, b = un.b, n = p.n_draft[b], L = p.len[b], two = it.mt == 2;
-  const int r = (warp & 3) * 32 + lane;
+  const int w = warp >> 2, b = un.b, n = p.n_draft[b], L = p.len[b], two = it.mt == 2, dup = un.dup;
+  const int r = (warp & 3) * 32 + lane, copy_rows = kTrRows / dup, copy = r / copy_rows;
   const int tile0 = un.rb * 2 * kTrNodes + (two ? w * kTrNodes : 0);  // first node of this row tile
-  const int node = tile0 + (r >> 3), h = g * kGroup + (r & 7);
-  const bool work = tile0 + (warp & 3) * 4 < n;  // some row of this warp is a node's
+  const int node = tile0 + ((r & (copy_rows - 1)) >> 3), h = g * kGroup + (r & 7);
+  const bool work = __any_sync(0xffffffffu, node < n);  // some row of this warp is a node's
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  const uint32_t* nans = reinterpret_cast<const uint32_t*>(smem + Lay<MT>::kNan);
+  const uint32_t* losts = reinterpret_cast<const uint32_t*>(smem + Y::kNan);
   const int steps = it.stream_steps(w);
 
   Row row;
@@ -620,112 +848,43 @@ __device__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, 
   row.hi = L;
   row.r0 = row.lo % kWindow;
   row.r1 = row.r0 + max(0, L - row.lo);
-  // positions that every row of the warp attends
-  const int lo_all = __reduce_max_sync(0xffffffffu, row.lo);
+  // from here on every node attends all of [.., L)
+  const int lo_all = p.window > 0 ? un.lo + kMaxTree : 0;
 
-  float m = -INFINITY, l = 0.f;  // m in log2 units, less kBias
+  const uint32_t mine = dup == 1 ? 15u : 3u << 2 * copy;
+  if (FP8) {
+    if (!warp_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, B)) return false;
+    const int e = reinterpret_cast<const int8_t*>(smem + Y::kQExp)[(two ? w * kTrRows : 0) + r];
+    scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&B->q_known));
+  }
+  float m = -INFINITY, l = 0.f;  // m in log2 units, less P's bias
   for (int s = 0; s < steps; ++s) {
-    const int ph = it.n[w] + s;
     const int ti = two ? s : 2 * s + w;  // tile of the item
-    if (!warp_wait(smem_u32(&B->s_full[w]), static_cast<uint32_t>(ph) & 1u, B)) return false;
+    if (!warp_wait(smem_u32(&B->s_full[w]), static_cast<uint32_t>(it.done(w) + s) & 1u, B)) return false;
     tc_fence_after();
     if (work) {
       const int t = it.t0 + ti, T = it.T + ti;
-      const uint32_t sp = lane_base + kColS + 128 * w, pp = lane_base + kColP + 128 * w;
-      // NaN in v: recorded when V is an operand
-      const int cv = 2 * T + 1;
-      if (!warp_wait(smem_u32(&B->ready[cv % NS]), static_cast<uint32_t>(cv / NS) & 1u, B)) return false;
-      const uint4 nan4 = *reinterpret_cast<const uint4*>(nans + (T % kInfo) * 4);
+      const uint32_t sp = lane_base + kColS + 128 * w, op = lane_base + kColO + 128 * w;
       const int s_lo = un.base + (2 * t - 1) * kHalf;
-      const bool plain = p.layout != FLINT_KV_RING && t > 0 && s_lo >= lo_all && s_lo + kTrKeys <= L &&
-                         (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
-      uint32_t mask[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-      uint32_t nan[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
-      if (!plain) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mask[k] = mask_word(p, un, row, t, k);
-          nan[k] &= mask[k];
-        }
-      }
-      auto load = [&](int k, uint32_t (&v)[32]) { tmem_ld32(sp + 32 * k, v); };
-      auto masked = [&](int k, uint32_t (&v)[32]) {
-        if (!plain) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = mask[k] >> i & 1u ? v[i] : 0xff800000u;
-            if (nan[k] >> i & 1u) v[i] = 0x7fc00000u;
-          }
-        }
-      };
-      uint32_t va[32], vb[32];
-      float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto maxima = [&](const uint32_t (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          mq[(i >> 1) & 3] = max3_nan(mq[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-      };
-      load(0, va);
-      load(1, vb);
-      tmem_wait_ld();
-      masked(0, va);
-      masked(1, vb);
-      maxima(va);
-      maxima(vb);
-      load(2, va);
-      load(3, vb);
-      tmem_wait_ld();
-      masked(2, va);
-      masked(3, vb);
-      maxima(va);
-      maxima(vb);
-      const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]) * scale - kBias;
-      float factor = 1.f;
-      const bool need = !(mx <= m + kTau) && mx != -INFINITY;  // (NaN needs)
-      if (need) {
-        factor = m == -INFINITY ? 0.f : ex2(m - mx);
-        m = mx;
-        l *= factor;
-      }
-      const float2 scale2 = make_float2(scale, scale), nmu = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      uint32_t pk[32];
-      auto probs = [&](const uint32_t (&v)[32], int at) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float2 x = fma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), scale2, nmu);
-          const float2 e = make_float2(ex2(x.x), ex2(x.y));
-          ls[c & 1] = add2(ls[c & 1], e);
-          const __half2 hp = __floats2half2_rn(e.x, e.y);
-          pk[at + c] = *reinterpret_cast<const uint32_t*>(&hp);
-        }
-      };
-      probs(va, 0);
-      probs(vb, 16);
-      tmem_st32(pp + 32, pk);  // keys 64..127 over S's last columns, which are read
-      load(0, va);
-      load(1, vb);
-      tmem_wait_ld();
-      masked(0, va);
-      masked(1, vb);
-      probs(va, 0);
-      probs(vb, 16);
-      const float2 lsum = add2(ls[0], ls[1]);
-      l += lsum.x + lsum.y;
-      tmem_st32(pp, pk);
-      if (s > 0 && __any_sync(0xffffffffu, need)) {
-        // O_w holds the stream's earlier steps: their PV completed before this S
-        const uint32_t op = lane_base + kColO + 128 * w;
+      if (p.layout == FLINT_KV_RING || t == 0 || s_lo < lo_all || s_lo + kTrKeys > L) {
+        // some key is not attended by some row: such scores become -inf, and NaN
+        // those of attended keys whose v is not finite (recorded when V is an operand)
+        if (!warp_wait(smem_u32(&B->v_ready[T & 3]), static_cast<uint32_t>(T >> 2) & 1u, B)) return false;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(op + 32 * c, va);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[32];
+          tmem_ld32(sp + 32 * k, v);
+          const uint32_t mask = mask_word(p, un, row, t, k), lost = (losts[(T % kInfo) * 8 + k] | (k < 2 ? losts[(T % kInfo) * 8 + 4 + k] : 0u)) & mask;
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * factor);
-          tmem_st32(op + 32 * c, va);
+          for (int i = 0; i < 32; ++i) v[i] = lost >> i & 1u ? 0x7fc00000u : mask >> i & 1u ? v[i] : 0xff800000u;
+          tmem_st32(sp + 32 * k, v);
         }
+        tmem_wait_st();
       }
-      tmem_wait_st();
+      softmax_step(sp, op, scale, mine, s == 0, m, l);
     }
     tc_fence_before();
     __syncwarp();
@@ -737,7 +896,7 @@ __device__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, 
   float a0 = 1.f, a1 = 0.f;
   int first = 0, chunks = 4;
   if (!two) {
-    float2* ex = reinterpret_cast<float2*>(smem + Lay<MT>::kEx);
+    float2* ex = reinterpret_cast<float2*>(smem + Y::kEx);
     ex[w * kTrRows + r] = make_float2(m, l);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&B->ex_full));
@@ -762,21 +921,15 @@ __device__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, 
     const bool both = !two && it.steps > 1;
 #pragma unroll 1
     for (int c = first; c < first + chunks; ++c) {
-      uint32_t v0[32];
+      uint32_t v0[32], v1[32];
       float o[32];
       tmem_ld32(lane_base + kColO + (two ? 128 * w : 0) + 32 * c, v0);
+      if (both) tmem_ld32(lane_base + kColO + 128 + 32 * c, v1);
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v0[i]);
-      if (!two) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= a0;
-        if (both) {
-          tmem_ld32(lane_base + kColO + 128 + 32 * c, v0);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(v0[i]), a1, o[i]);
-        }
+      for (int i = 0; i < 32; ++i) {
+        o[i] = __uint_as_float(v0[i]) * a0;
+        if (both) o[i] = fmaf(__uint_as_float(v1[i]), a1, o[i]);
       }
       if (node < n) {
         if (whole) {
@@ -806,7 +959,8 @@ __device__ bool softmax_item(const TreeParams& p, const Item& it, int q, int g, 
 template <int MT, bool FP8>
 __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  Bars* B = reinterpret_cast<Bars*>(smem + Lay<MT>::kBar);
+  using Y = Lay<MT, FP8>;
+  Bars* B = reinterpret_cast<Bars*>(smem + Y::kBar);
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = blockIdx.x / kKvHeads, g = blockIdx.x % kKvHeads;
@@ -816,21 +970,32 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
+      B->armed[s] = 0;
       mbar_init(smem_u32(&B->full[s]), 1);
-      mbar_init(smem_u32(&B->ready[s]), kConvWarps);
       mbar_init(smem_u32(&B->empty[s]), 1);
     }
+    for (int s = 0; s < 4; ++s) {
+      B->raw_armed[s] = 0;
+      mbar_init(smem_u32(&B->raw_full[s]), 1);
+      mbar_init(smem_u32(&B->raw_free[s]), kConvWarps);
+      mbar_init(smem_u32(&B->v_ready[s]), kConvWarps);
+    }
     for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&B->v_empty[w]), 1);
       mbar_init(smem_u32(&B->s_full[w]), 1);
       mbar_init(smem_u32(&B->p_ready[w]), 4);
     }
-    mbar_init(smem_u32(&B->q_ready), kConvWarps);
+    mbar_init(smem_u32(&B->kd_ready), kConvWarps);
+    mbar_init(smem_u32(&B->q_full), 1);
     mbar_init(smem_u32(&B->q_empty), 1);
+    mbar_init(smem_u32(&B->q_ready), kConvWarps);
+    mbar_init(smem_u32(&B->q_known), kSoftWarps);
     mbar_init(smem_u32(&B->o_full), 1);
     mbar_init(smem_u32(&B->o_free), kSoftWarps);
     mbar_init(smem_u32(&B->ex_full), kSoftWarps);
     mbar_init(smem_u32(&B->mma_done), 1);
     B->abort = 0;
+    B->q_armed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
   }
@@ -845,34 +1010,41 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = B->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B->tmem_base, 0);
 
-  int armed = 0;
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoft));
     const float scale = FP8 ? kTrScale * p.k_scale[g] : kTrScale;
     Item it;
     for (bool more = first_item(p, q, it); more; more = next_item(p, q, it))
-      if (!softmax_item<MT>(p, it, q, g, scale, tmem, smem, B, warp, lane)) {
+      if (!softmax_item<MT, FP8>(p, it, q, g, scale, tmem, smem, B, warp, lane)) {
         if (lane == 0) raise_abort(p, B);
         break;
       }
   } else if (warp < kTmaWarp) {
-    run_conv<MT, FP8>(p, q, g, base, smem, B, threadIdx.x - kSoftWarps * 32);
-  } else if (warp == kTmaWarp) {
-    armed = run_tma<MT, FP8>(p, q, g, base, B, lane);
-  } else if (lane == 0) {
-    run_mma<MT, FP8>(p, q, base, tmem, B);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConv));
+    if (!run_conv<MT, FP8>(p, q, g, smem, B, threadIdx.x - kSoftWarps * 32) && lane == 0) raise_abort(p, B);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
+    if (warp == kTmaWarp && !run_tma<MT, FP8, false>(p, q, g, base, B, lane) && lane == 0) raise_abort(p, B);
+    if (warp == kTmaWarpV && !run_tma<MT, FP8, true>(p, q, g, base, B, lane) && lane == 0) raise_abort(p, B);
+    if (warp == kMmaWarp) run_mma<MT, FP8>(p, q, base, tmem, B, lane);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kTmaWarp && lane == 0 && aborted(B)) {
-    // copies in flight land before the CTA's shared memory goes away: the last
-    // kStages stages armed (an earlier one was consumed, so it landed)
-    constexpr int NS = Lay<MT>::kStages;
+    // copies in flight land before the CTA's shared memory goes away: Q and the
+    // last of each stage (an earlier one was consumed, so it landed)
     const unsigned long long t0 = globaltimer_ns();
-    for (int c = max(0, armed - NS); c < armed; ++c)
-      while (!mbar_try_wait(smem_u32(&B->full[c % NS]), static_cast<uint32_t>(c / NS) & 1u))
+    auto land = [&](uint64_t* bar, int c) {
+      while (!mbar_try_wait(smem_u32(bar), static_cast<uint32_t>(c) & 1u))
         if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+    };
+    if (B->q_armed > 0) land(&B->q_full, B->q_armed - 1);
+    for (int st = 0; st < Y::kTiles; ++st)
+      if (B->armed[st] > 0) land(&B->full[st], (B->armed[st] - 1) / Y::kTiles);
+    for (int st = 0; st < Y::kRaws; ++st)
+      if (B->raw_armed[st] > 0) land(&B->raw_full[st], (B->raw_armed[st] - 1) / Y::kRaws);
   }
   if (warp == kMmaWarp) {
     __syncwarp();
@@ -881,40 +1053,76 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   }
 }
 
-// Joins the partials of the units that were cut: a CTA per (unit, node, KV
-// head), thread (row of 8, chunk of 4 dims); with M = max m_p,
-//     out = sum_p 2^(m_p - M) O_p / (sum_p 2^(m_p - M) l_p + 2^(sink - M)).
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Joins the partials of the units that left some: a CTA per (unit, node, KV
+// head, 32 dims); thread (row of 8, chunk of 4 dims, share of the partials); with
+// M = max m_k,
+//     out = sum_k 2^(m_k - M) O_k / (sum_k 2^(m_k - M) l_k + 2^(sink - M)).
+// Partial k is copy k % dup of the unit's k / dup-th group.  Bound by the
+// latency of its loads: the weights once, then up to kJoinShares partials at a
+// time by as many thread groups.
+constexpr int kJoinShares = 4, kJoinThreads = kGroup * 8 * kJoinShares;
+constexpr int kJoinMax = kMaxTreeGroups * 2;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float wt[kJoinMax][kGroup];   // m, then 2^(m - M)
+  __shared__ float ltot[kGroup], mtop[kGroup];
+  __shared__ float4 sum[kJoinShares - 1][kGroup * 8];
   const int g = blockIdx.x % kKvHeads, u = blockIdx.z;
   const TreeUnit& un = p.unit[u];
   const int nd = blockIdx.x / kKvHeads, b = un.b, node = un.rb * 2 * kTrNodes + nd;
-  if (un.q0 == un.q1 || node >= p.n_draft[b]) return;
-  const int row = threadIdx.x & 7, c = threadIdx.x >> 3, r = (nd & (kTrNodes - 1)) * kGroup + row;
-  auto part = [&](int q) {
-    const int slot = p.cut[q].unit == u ? 0 : 1;
-    return p.partials + ((static_cast<long long>(q) * kKvHeads + g) * 4 + slot * 2 + (nd >> 4)) * kTreePartialFloats;
+  const int q0 = un.q0, shift = un.dup >> 1;  // dup 1, 2: 0, 1
+  if (q0 == un.q1 || node >= p.n_draft[b]) return;
+  const int parts = (un.q1 - q0 + 1) << shift;
+  const int r0 = (nd & (kTrNodes - 1)) * kGroup;
+  // only the unit's first group may hold it as a later item than its first
+  const int slot0 = p.cut[q0].unit == u ? 0 : 1;
+  const float* base = p.partials + (static_cast<long long>(g) * 4 + (nd >> 4)) * kTreePartialFloats;
+  auto part = [&](int k) {
+    const int q = k >> shift;
+    return base + (static_cast<long long>(q0 + q) * kKvHeads * 4 + (q == 0 ? slot0 * 2 : 0)) * kTreePartialFloats;
   };
-  float M = -INFINITY;
-  bool nan = false;
-  for (int q = un.q0; q <= un.q1; ++q) {
-    const float m = part(q)[kTrRows * kDim + r];
-    nan |= m != m;
-    M = fmaxf(M, m);
+  auto row_of = [&](int k, int row) { return r0 + row + (k & ((1 << shift) - 1)) * (kTrRows >> shift); };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int x = threadIdx.x; x < parts * kGroup; x += kJoinThreads)
+    wt[x >> 3][x & 7] = part(x >> 3)[kTrRows * kDim + row_of(x >> 3, x & 7)];
+  __syncthreads();
+  {  // a warp per row
+    const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) M = max3_nan(M, wt[k][row], wt[k][row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = max3_nan(M, __shfl_xor_sync(0xffffffffu, M, o), M);
+    float l = 0.f;
+    for (int k = lane; k < parts; k += 32) {
+      const float m = wt[k][row], e = m == -INFINITY ? 0.f : ex2(m - M);
+      wt[k][row] = e;
+      l = fmaf(part(k)[kTrRows * kDim + kTrRows + row_of(k, row)], e, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      ltot[row] = l;
+      mtop[row] = M;
+    }
   }
-  if (nan) M = NAN;
+  __syncthreads();
+  const int row = threadIdx.x & 7, c = blockIdx.y * 8 + (threadIdx.x >> 3 & 7), share = threadIdx.x >> 6;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int q = un.q0; q <= un.q1; ++q) {
-    const float* x = part(q);
-    const float m = x[kTrRows * kDim + r], wt = m == -INFINITY ? 0.f : ex2(m - M);
-    l = fmaf(x[kTrRows * kDim + kTrRows + r], wt, l);
-    const float4 y = reinterpret_cast<const float4*>(x)[c * kTrRows + r];
-    o = make_float4(fmaf(y.x, wt, o.x), fmaf(y.y, wt, o.y), fmaf(y.z, wt, o.z), fmaf(y.w, wt, o.w));
+#pragma unroll 8
+  for (int k = share; k < parts; k += kJoinShares) {
+    const float e = wt[k][row];
+    const float4 y = reinterpret_cast<const float4*>(part(k))[c * kTrRows + row_of(k, row)];
+    o = make_float4(fmaf(y.x, e, o.x), fmaf(y.y, e, o.y), fmaf(y.z, e, o.z), fmaf(y.w, e, o.w));
+  }
+  if (share > 0) sum[share - 1][threadIdx.x & 63] = o;
+  __syncthreads();
+  if (share > 0) return;
+#pragma unroll
+  for (int k = 0; k < kJoinShares - 1; ++k) {
+    const float4 y = sum[k][threadIdx.x];
+    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
   }
   const int h = g * kGroup + row;
-  const float sc = (p.fp8 ? p.v_scale[g] : 1.f) / (l + ex2(p.sinks[h] * kTrLog2e - M));
+  const float sc = (p.fp8 ? p.v_scale[g] : 1.f) / (ltot[row] + ex2(p.sinks[h] * kTrLog2e - mtop[row]));
   reinterpret_cast<uint2*>(p.out + ((static_cast<long long>(b) * p.N + node) * kHeads + h) * kDim)[c] =
       make_uint2(pack_bf16x2(o.x * sc, o.y * sc), pack_bf16x2(o.z * sc, o.w * sc));
 }
@@ -922,9 +1130,9 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 template <int MT, bool FP8>
 cudaError_t launch_one(const TreeParams& p, cudaStream_t stream) {
   static ContextSet configured;
-  const cudaError_t e = configure_once(configured, reinterpret_cast<const void*>(tree_kernel<MT, FP8>), static_cast<int>(Lay<MT>::kBytes));
+  const cudaError_t e = configure_once(configured, reinterpret_cast<const void*>(tree_kernel<MT, FP8>), static_cast<int>(Lay<MT, FP8>::kBytes));
   if (e != cudaSuccess) return e;
-  tree_kernel<MT, FP8><<<p.n_groups * kKvHeads, kTrThreads, Lay<MT>::kBytes, stream>>>(p);
+  tree_kernel<MT, FP8><<<p.n_groups * kKvHeads, kTrThreads, Lay<MT, FP8>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -981,6 +1189,8 @@ void plan_tree(TreeParams& p, int num_groups) {
     }
     p.unit[x].q0 = static_cast<int16_t>(q0);
     p.unit[x].q1 = static_cast<int16_t>(q1);
+    const int nodes = p.n_draft[p.unit[x].b] - p.unit[x].rb * 2 * kTrNodes;
+    p.unit[x].dup = q1 == q0 || nodes > kTrNodes / 2 ? 1 : 2;
     if (q1 > q0) p.split = 1;
   }
 }
@@ -999,8 +1209,8 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   // The second launch's set-up overlaps the first kernel; it waits for that
   // kernel's end before it reads.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(nodes, 2 * kTrNodes) * kKvHeads, 1, p.n_units);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(std::min(nodes, 2 * kTrNodes) * kKvHeads, 4, p.n_units);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
