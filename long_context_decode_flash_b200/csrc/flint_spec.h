@@ -107,6 +107,7 @@ struct TreeParams {
   const int32_t* table;
   int32_t layout, max_blocks, num_blocks, fp8;
   float k_scale[4], v_scale[4];
+  double k_inv[4], v_inv[4];   // 1 / scale
   int32_t len[FLINT_MAX_BATCH];
   int8_t n_draft[FLINT_MAX_BATCH];
   int32_t N, B, window;

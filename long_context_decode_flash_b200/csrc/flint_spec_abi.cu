@@ -210,6 +210,8 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   for (int g = 0; g < kKvHeads; ++g) {
     p.k_scale[g] = c.k_scale[g];
     p.v_scale[g] = c.v_scale[g];
+    p.k_inv[g] = p.fp8 ? 1.0 / c.k_scale[g] : 0.0;
+    p.v_inv[g] = p.fp8 ? 1.0 / c.v_scale[g] : 0.0;
   }
   p.N = N;
   p.B = B;

@@ -197,10 +197,18 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// fp16 pairs with what is not finite made 0.
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
-  if ((x & 0x7C00u) == 0x7C00u) x &= 0xFFFF0000u;
-  if ((x & 0x7C000000u) == 0x7C000000u) x &= 0xFFFFu;
+// An fp16 pair with infinities made +-65504 and, where `clear`, NaN made 0;
+// any NaN sets `nan`.
+__device__ __forceinline__ uint32_t mend_pair(uint32_t x, bool clear, bool& nan) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 16) {
+    const uint32_t mag = x >> e & 0x7FFFu;
+    if (mag == 0x7C00u) x -= 1u << e;
+    if (mag > 0x7C00u) {
+      nan = true;
+      if (clear) x &= ~(0xFFFFu << e);
+    }
+  }
   return x;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -381,67 +389,83 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (c >> 3) * kDimHalf + r * 128 + ((c ^ r) & 7) * 16;
 }
 __device__ __forceinline__ uint4& smem4(uint8_t* p) { return *reinterpret_cast<uint4*>(p); }
-// Two floats -> packed f16x2 (first in the low half), nearest even, saturating
-// at +-65504; NaN stays NaN.
-__device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
+__device__ __forceinline__ uint32_t bf16x2_to_f16(uint32_t w) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v) {
-  return make_uint4(f16x2_sat(bf16_lo(v.x), bf16_hi(v.x)), f16x2_sat(bf16_lo(v.y), bf16_hi(v.y)),
-                    f16x2_sat(bf16_lo(v.z), bf16_hi(v.z)), f16x2_sat(bf16_lo(v.w), bf16_hi(v.w)));
+  return make_uint4(bf16x2_to_f16(v.x), bf16x2_to_f16(v.y), bf16x2_to_f16(v.z), bf16x2_to_f16(v.w));
 }
-// The codes that an E4M3 cache of this scale holds for two bf16 values.
-__device__ __forceinline__ uint32_t bf16x2_to_e4m3(uint32_t w, float scale) {
-  return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(w), scale), __fdiv_rn(bf16_hi(w), scale));
+// The codes that an E4M3 cache holds for two bf16 values, from the reciprocal of
+// its scale in double: x / scale rounded to float, then to E4M3.  The product in
+// double is within 2^-52 of the quotient, and a quotient of 8 by 24 bits that is
+// not a midpoint of floats (25 bits) is at least 2^-49 away from one: the float is
+// the rounded quotient.  (A float division measured several times as long.)
+__device__ __forceinline__ uint32_t bf16x2_to_e4m3(uint32_t w, double inv) {
+  return f32x2_to_e4m3x2(static_cast<float>(bf16_lo(w) * inv), static_cast<float>(bf16_hi(w) * inv));
+}
+// acc + 0 * x per half: a half of acc turns NaN where x is not finite (fp16).
+__device__ __forceinline__ uint32_t nan_acc(uint32_t acc, uint4 x) {
+  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.x), "r"(0u));
+  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.y), "r"(0u));
+  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.z), "r"(0u));
+  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.w), "r"(0u));
+  return acc;
 }
 
-// What is not finite in a 16-byte chunk made 0; true if there was any.
-__device__ __forceinline__ bool make_finite(uint4& v) {
-  const uint4 f = make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
-  const bool any = f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
-  v = f;
-  return any;
+__device__ __forceinline__ uint4 mend(uint4 v, bool clear, bool& nan) {
+  return make_uint4(mend_pair(v.x, clear, nan), mend_pair(v.y, clear, nan), mend_pair(v.z, clear, nan), mend_pair(v.w, clear, nan));
 }
 
 // A warp's 32 rows of a Q tile, bf16, into two E4M3 terms in place: with 2^e the
 // power of two that brings a row's largest magnitude into [128, 256), q 2^e = t1
 // + t2 up to 2^-10 (exact for magnitudes down to 2^-9 of the largest: bf16 has 8
 // bits, each term 4).  t1's 128 codes take the first 64-dim half's row, t2's the
-// second's.  Two rows at a time, 16 lanes each.  exps gets e; a row with
+// second's.  Two rows at a time, 16 lanes each, four times over.  exps gets e; a row with
 // something not finite becomes NaN.
 __device__ __forceinline__ void split_q_rows(uint8_t* tile, int row0, int8_t* exps, int lane) {
   const int c = lane & 15;
-#pragma unroll 2
-  for (int i = 0; i < 16; ++i) {
-    const int r = row0 + 2 * i + (lane >> 4);
-    const uint4 y = smem4(tile + chunk_at(r, c));
-    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-    float top = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16; i0 += 4) {
+    uint2 t1[4], t2[4];
+    int exp[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = max3_nan(top, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
+    for (int i = 0; i < 4; ++i) {
+      const uint4 y = smem4(tile + chunk_at(row0 + 2 * (i0 + i) + (lane >> 4), c));
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+      // magnitudes of bf16 order as integers, NaN above all
+      uint32_t top = 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max3_nan(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
-    const int field = static_cast<int>(__float_as_uint(top) >> 23 & 255u);  // biased exponent
-    const int e = field == 0 ? 0 : min(126, 134 - field);                 // (a row of 0 or subnormal: any)
-    const float up = field == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    uint32_t t1[2], t2[2];
+      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float a = bf16_lo(w[2 * k]) * up, b = bf16_hi(w[2 * k]) * up;
-      const float u = bf16_lo(w[2 * k + 1]) * up, v = bf16_hi(w[2 * k + 1]) * up;
-      t1[k] = f32x2_to_e4m3x2(a, b) | f32x2_to_e4m3x2(u, v) << 16;
-      uint32_t lo, hi;
-      e4m3x4_to_f16x2x2(t1[k], lo, hi);
-      const float2 ab = __half22float2(*reinterpret_cast<__half2*>(&lo)), uv = __half22float2(*reinterpret_cast<__half2*>(&hi));
-      t2[k] = f32x2_to_e4m3x2(a - ab.x, b - ab.y) | f32x2_to_e4m3x2(u - uv.x, v - uv.y) << 16;
+      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int field = static_cast<int>(top >> 7);           // biased exponent
+      exp[i] = field == 0 ? 0 : min(126, 134 - field);        // (a row of 0 or subnormal: any)
+      const float up = field == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 + exp[i]) << 23);
+      uint32_t a1[2], a2[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float a = bf16_lo(w[2 * k]) * up, b = bf16_hi(w[2 * k]) * up;
+        const float u = bf16_lo(w[2 * k + 1]) * up, v = bf16_hi(w[2 * k + 1]) * up;
+        a1[k] = f32x2_to_e4m3x2(a, b) | f32x2_to_e4m3x2(u, v) << 16;
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2x2(a1[k], lo, hi);
+        const float2 ab = __half22float2(*reinterpret_cast<__half2*>(&lo)), uv = __half22float2(*reinterpret_cast<__half2*>(&hi));
+        a2[k] = f32x2_to_e4m3x2(a - ab.x, b - ab.y) | f32x2_to_e4m3x2(u - uv.x, v - uv.y) << 16;
+      }
+      t1[i] = make_uint2(a1[0], a1[1]);
+      t2[i] = make_uint2(a2[0], a2[1]);
     }
-    __syncwarp();  // both rows are read
-    uint8_t* at = tile + chunk_at(r, c >> 1) + (c & 1) * 8;
-    *reinterpret_cast<uint2*>(at) = make_uint2(t1[0], t1[1]);
-    *reinterpret_cast<uint2*>(at + kDimHalf) = make_uint2(t2[0], t2[1]);
-    if (c == 0) exps[r] = static_cast<int8_t>(e);
+    __syncwarp();  // these rows are read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + 2 * (i0 + i) + (lane >> 4);
+      uint8_t* at = tile + chunk_at(r, c >> 1) + (c & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = t1[i];
+      *reinterpret_cast<uint2*>(at + kDimHalf) = t2[i];
+      if (c == 0) exps[r] = static_cast<int8_t>(exp[i]);
+    }
   }
 }
 
@@ -489,15 +513,15 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
         if (!raw_wait() || !warp_wait(smem_u32(&B->full[c % Y::kTiles]), static_cast<uint32_t>(c / Y::kTiles) & 1u, B)) return false;
         const uint8_t* from = raw_stage() + (ct >> 6) * kBox16 + j * 128;
         uint8_t* to = smem + Y::kTile + (c % Y::kTiles) * kCodes + j * 128;
-        const float scale = p.k_scale[g];
+        const double inv = p.k_inv[g];
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {  // 16 values, one chunk of codes
           uint32_t code[4];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint4 y = *reinterpret_cast<const uint4*>(from + (((2 * i + k) ^ j) & 7) * 16);
-            code[2 * k] = bf16x2_to_e4m3(y.x, scale) | bf16x2_to_e4m3(y.y, scale) << 16;
-            code[2 * k + 1] = bf16x2_to_e4m3(y.z, scale) | bf16x2_to_e4m3(y.w, scale) << 16;
+            code[2 * k] = bf16x2_to_e4m3(y.x, inv) | bf16x2_to_e4m3(y.y, inv) << 16;
+            code[2 * k + 1] = bf16x2_to_e4m3(y.z, inv) | bf16x2_to_e4m3(y.w, inv) << 16;
           }
           smem4(to + (((4 * (ct >> 6) + i) ^ j) & 7) * 16) = make_uint4(code[0], code[1], code[2], code[3]);
         }
@@ -531,29 +555,30 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
       }
       uint8_t* tile;
       uint32_t half_rows = 0;  // record of the drafts' rows' second halves
-      bool has = false;  // something in the row was not finite
+      bool has = false;   // the row held NaN, and it is for the record
+      uint32_t bad = 0;   // an fp16 pair, NaN if so
       if (FP8) {
         tile = smem + Y::kV + (T % Y::kVs) * kStage;
         if (T >= Y::kVs && !warp_wait(smem_u32(&B->v_empty[T % Y::kVs]), static_cast<uint32_t>(T / Y::kVs - 1) & 1u, B)) return false;
         if (t == 0) {  // the drafts, half a row a thread
           if (!raw_wait()) return false;
           const uint8_t* from = raw_stage() + (ct >> 6) * kBox16 + j * 128;
-          const float scale = p.v_scale[g];
-          bool bad = false;
+          const double inv = p.v_inv[g];
+          bool lost_half = false;
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const uint4 y = *reinterpret_cast<const uint4*>(from + ((i ^ j) & 7) * 16);
             uint4 z = make_uint4(0, 0, 0, 0);
             if (j < nd) {
-              const uint32_t a = bf16x2_to_e4m3(y.x, scale) | bf16x2_to_e4m3(y.y, scale) << 16;
-              const uint32_t d = bf16x2_to_e4m3(y.z, scale) | bf16x2_to_e4m3(y.w, scale) << 16;
+              const uint32_t a = bf16x2_to_e4m3(y.x, inv) | bf16x2_to_e4m3(y.y, inv) << 16;
+              const uint32_t d = bf16x2_to_e4m3(y.z, inv) | bf16x2_to_e4m3(y.w, inv) << 16;
               e4m3x4_to_f16x2x2(a, z.x, z.y);
               e4m3x4_to_f16x2x2(d, z.z, z.w);
             }
-            bad |= make_finite(z);
+            z = mend(z, true, lost_half);
             smem4(tile + chunk_at(j, 8 * (ct >> 6) + i)) = z;
           }
-          half_rows = __ballot_sync(0xffffffffu, bad);
+          half_rows = __ballot_sync(0xffffffffu, lost_half);
           raw_done();
         }
         if (!raw_wait()) return false;
@@ -570,6 +595,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
             e4m3x4_to_f16x2x2(code[k].y, a.z, a.w);
             e4m3x4_to_f16x2x2(code[k].z, d.x, d.y);
             e4m3x4_to_f16x2x2(code[k].w, d.z, d.w);
+            bad = nan_acc(nan_acc(bad, a), d);
             smem4(tile + chunk_at(ct, 2 * k)) = a;
             smem4(tile + chunk_at(ct, 2 * k + 1)) = d;
           }
@@ -584,19 +610,22 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
 #pragma unroll
           for (int k = 0; k < 8; ++k) y[k] = smem4(tile + chunk_at(ct, 8 * x + k));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) smem4(tile + chunk_at(ct, 8 * x + k)) = token ? bf16x8_to_f16(y[k]) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) {
+            y[k] = token ? bf16x8_to_f16(y[k]) : make_uint4(0, 0, 0, 0);
+            bad = nan_acc(bad, y[k]);
+            smem4(tile + chunk_at(ct, 8 * x + k)) = y[k];
+          }
         }
       }
-      if (scan && !(FP8 && h == 0)) {
-        // What is not finite becomes 0, for the rows that do not attend the
-        // key; the rows that do learn of it by the record.
+      if (bad & 0x7FFF7FFFu) {
+        // Infinities saturate.  NaN becomes 0 where some rows do not attend the
+        // key; the rows that do learn of it by the record.  (Where all do, it
+        // stays.)
 #pragma unroll 1
         for (int k = 0; k < 16; ++k) {
-          uint4 y = smem4(tile + chunk_at(ct, k));
-          if (make_finite(y)) {
-            has = true;
-            smem4(tile + chunk_at(ct, k)) = y;
-          }
+          bool nan = false;
+          smem4(tile + chunk_at(ct, k)) = mend(smem4(tile + chunk_at(ct, k)), scan, nan);
+          has |= nan && scan;
         }
       }
       const uint32_t word = __ballot_sync(0xffffffffu, has);
@@ -1010,6 +1039,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The set-up above overlaps the end of the launch before; what that one wrote
+  // is there from here on.  The join may be set up as CTAs end.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, B->tmem_base, 0);
 
   if (warp < kSoftWarps) {
@@ -1058,12 +1091,13 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
 // M = max m_k,
 //     out = sum_k 2^(m_k - M) O_k / (sum_k 2^(m_k - M) l_k + 2^(sink - M)).
 // Partial k is copy k % dup of the unit's k / dup-th group.  Bound by the
-// latency of its loads: the weights once, then up to kJoinShares partials at a
-// time by as many thread groups.
-constexpr int kJoinShares = 4, kJoinThreads = kGroup * 8 * kJoinShares;
+// latency of its loads: the weights once, then O's of as many
+// partials at once as kJoinShares thread groups hold.
+constexpr int kJoinShares = 8, kJoinThreads = kGroup * 8 * kJoinShares;
 constexpr int kJoinMax = kMaxTreeGroups * 2;
+static_assert(kJoinThreads >= kGroup * 32, "a warp per row");
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ float wt[kJoinMax][kGroup];   // m, then 2^(m - M)
+  __shared__ float2 wt[kJoinMax][kGroup];  // m (then 2^(m - M)), l
   __shared__ float ltot[kGroup], mtop[kGroup];
   __shared__ float4 sum[kJoinShares - 1][kGroup * 8];
   const int g = blockIdx.x % kKvHeads, u = blockIdx.z;
@@ -1081,45 +1115,60 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     return base + (static_cast<long long>(q0 + q) * kKvHeads * 4 + (q == 0 ? slot0 * 2 : 0)) * kTreePartialFloats;
   };
   auto row_of = [&](int k, int row) { return r0 + row + (k & ((1 << shift) - 1)) * (kTrRows >> shift); };
+  const int row = threadIdx.x & 7, c = blockIdx.y * 8 + (threadIdx.x >> 3 & 7), share = threadIdx.x >> 6;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int x = threadIdx.x; x < parts * kGroup; x += kJoinThreads)
-    wt[x >> 3][x & 7] = part(x >> 3)[kTrRows * kDim + row_of(x >> 3, x & 7)];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // all first loads of O and those of m and l are in flight together
+  constexpr int kAhead = 10;
+  float4 y[kAhead];
+  auto load = [&](int k) { return reinterpret_cast<const float4*>(part(k))[c * kTrRows + row_of(k, row)]; };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int k = share + i * kJoinShares;
+    y[i] = k < parts ? load(k) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int x = threadIdx.x; x < parts * kGroup; x += kJoinThreads) {
+    const float* ml = part(x >> 3) + kTrRows * kDim + row_of(x >> 3, x & 7);
+    wt[x >> 3][x & 7] = make_float2(ml[0], ml[kTrRows]);
+  }
   __syncthreads();
-  {  // a warp per row
-    const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kGroup * 32) {  // a warp per row
+    const int wr = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float M = -INFINITY;
-    for (int k = lane; k < parts; k += 32) M = max3_nan(M, wt[k][row], wt[k][row]);
+    for (int k = lane; k < parts; k += 32) M = max3_nan(M, wt[k][wr].x, wt[k][wr].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = max3_nan(M, __shfl_xor_sync(0xffffffffu, M, o), M);
     float l = 0.f;
     for (int k = lane; k < parts; k += 32) {
-      const float m = wt[k][row], e = m == -INFINITY ? 0.f : ex2(m - M);
-      wt[k][row] = e;
-      l = fmaf(part(k)[kTrRows * kDim + kTrRows + row_of(k, row)], e, l);
+      const float2 ml = wt[k][wr];
+      const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      wt[k][wr].x = e;
+      l = fmaf(ml.y, e, l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      ltot[row] = l;
-      mtop[row] = M;
+      ltot[wr] = l;
+      mtop[wr] = M;
     }
   }
   __syncthreads();
-  const int row = threadIdx.x & 7, c = blockIdx.y * 8 + (threadIdx.x >> 3 & 7), share = threadIdx.x >> 6;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = share; k < parts; k += kJoinShares) {
-    const float e = wt[k][row];
-    const float4 y = reinterpret_cast<const float4*>(part(k))[c * kTrRows + row_of(k, row)];
-    o = make_float4(fmaf(y.x, e, o.x), fmaf(y.y, e, o.y), fmaf(y.z, e, o.z), fmaf(y.w, e, o.w));
-  }
+  auto add = [&](int k, const float4& v) {
+    const float e = wt[k][row].x;
+    o = make_float4(fmaf(v.x, e, o.x), fmaf(v.y, e, o.y), fmaf(v.z, e, o.z), fmaf(v.w, e, o.w));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (share + i * kJoinShares < parts) add(share + i * kJoinShares, y[i]);
+  for (int k = share + kAhead * kJoinShares; k < parts; k += kJoinShares) add(k, load(k));
   if (share > 0) sum[share - 1][threadIdx.x & 63] = o;
   __syncthreads();
   if (share > 0) return;
 #pragma unroll
   for (int k = 0; k < kJoinShares - 1; ++k) {
-    const float4 y = sum[k][threadIdx.x];
-    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+    const float4 v = sum[k][threadIdx.x];
+    o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
   }
   const int h = g * kGroup + row;
   const float sc = (p.fp8 ? p.v_scale[g] : 1.f) / (ltot[row] + ex2(p.sinks[h] * kTrLog2e - mtop[row]));
@@ -1127,16 +1176,36 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       make_uint2(pack_bf16x2(o.x * sc, o.y * sc), pack_bf16x2(o.z * sc, o.w * sc));
 }
 
+// Launches that overlap their set-up with the end of the launch before
+// (griddepcontrol.wait comes before anything is read or written).
+cudaError_t launch_overlapped(dim3 grid, int threads, size_t smem, cudaStream_t stream, void (*kernel)(TreeParams), const TreeParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int MT, bool FP8>
 cudaError_t launch_one(const TreeParams& p, cudaStream_t stream) {
   static ContextSet configured;
-  const cudaError_t e = configure_once(configured, reinterpret_cast<const void*>(tree_kernel<MT, FP8>), static_cast<int>(Lay<MT, FP8>::kBytes));
+  constexpr size_t bytes = Lay<MT, FP8>::kBytes;
+  const cudaError_t e = configure_once(configured, reinterpret_cast<const void*>(tree_kernel<MT, FP8>), static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  tree_kernel<MT, FP8><<<p.n_groups * kKvHeads, kTrThreads, Lay<MT, FP8>::kBytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(dim3(p.n_groups * kKvHeads), kTrThreads, bytes, stream, tree_kernel<MT, FP8>, p);
 }
 
 }  // namespace
+
+// What the beginning of a unit costs a CTA, in tiles (its Q, its drafts, and the
+// end of the unit before).
+constexpr int kUnitCost = 2;
 
 void plan_tree(TreeParams& p, int num_groups) {
   // Units, and what a tile of each costs: with E4M3 a tile is bound by the
@@ -1158,7 +1227,7 @@ void plan_tree(TreeParams& p, int num_groups) {
       u.tiles = (u.halves + 1) / 2;
       cost[n_units] = p.fp8 ? u.mt : 1;
       begin[n_units] = total;
-      total += cost[n_units] * u.tiles;
+      total += cost[n_units] * u.tiles + kUnitCost;
       ++n_units;
     }
   }
@@ -1169,7 +1238,7 @@ void plan_tree(TreeParams& p, int num_groups) {
   for (int k = 0; k <= num_groups; ++k) {
     const int64_t at = total * k / num_groups;
     while (u < n_units && begin[u + 1] <= at) ++u;
-    const TreeCut c{static_cast<int16_t>(u), static_cast<int16_t>(u < n_units ? (at - begin[u]) / cost[u] : 0)};
+    const TreeCut c{static_cast<int16_t>(u), static_cast<int16_t>(u < n_units ? std::max<int64_t>(0, at - begin[u] - kUnitCost) / cost[u] : 0)};
     if (groups > 0 && p.cut[groups - 1].unit == c.unit && p.cut[groups - 1].tile == c.tile) continue;
     p.cut[groups++] = c;
   }
@@ -1206,18 +1275,7 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   const cudaError_t e = two ? (p.fp8 ? launch_one<2, true>(p, stream) : launch_one<2, false>(p, stream))
                             : (p.fp8 ? launch_one<1, true>(p, stream) : launch_one<1, false>(p, stream));
   if (e != cudaSuccess || !p.split) return e;
-  // The second launch's set-up overlaps the first kernel; it waits for that
-  // kernel's end before it reads.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(nodes, 2 * kTrNodes) * kKvHeads, 4, p.n_units);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel, p);
+  return launch_overlapped(dim3(std::min(nodes, 2 * kTrNodes) * kKvHeads, 4, p.n_units), kJoinThreads, 0, stream, tree_join_kernel, p);
 }
 
 }  // namespace flint
