@@ -66,7 +66,7 @@ struct VerifyParams {
   int32_t B, N, V;
   int8_t n_draft[FLINT_MAX_BATCH];
 };
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams& p, int num_sms, cudaStream_t stream);
 
 // ---- flint_attn_tree ----------------------------------------------------------------
 // A partial: O of 128 rows (16 nodes x 8 heads), m and l, fp32.  A CTA may leave

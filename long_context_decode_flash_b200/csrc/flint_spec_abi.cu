@@ -266,7 +266,9 @@ flint_status flint_verify_tree(const float* target, int64_t target_stride, const
   p.B = B;
   p.N = N;
   p.V = V;
-  return launched(launch_verify(p, static_cast<cudaStream_t>(stream)), who);
+  int sms = 0;
+  if (device_num_sms(&sms) != 0) return record_error(FLINT_ERR_CUDA, "%s: cannot read the device's SM count", who);
+  return launched(launch_verify(p, sms, static_cast<cudaStream_t>(stream)), who);
 }
 
 flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_layers, const int32_t* path,
