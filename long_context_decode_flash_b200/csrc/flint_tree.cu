@@ -1243,24 +1243,18 @@ void plan_tree(TreeParams& p, int num_groups) {
     p.cut[groups++] = c;
   }
   p.n_groups = groups - 1;
+  // the groups with a share of each unit (no group is empty: they are a range)
   p.split = 0;
+  int q = 0;
   for (int x = 0; x < n_units; ++x) {
-    // the groups with a share of unit x
-    int q0 = p.n_groups, q1 = -1;
-    for (int q = 0; q < p.n_groups; ++q) {
-      const TreeCut a = p.cut[q], e = p.cut[q + 1];
-      const int t0 = a.unit < x ? 0 : a.unit == x ? a.tile : p.unit[x].tiles;
-      const int t1 = e.unit > x ? p.unit[x].tiles : e.unit == x ? e.tile : 0;
-      if (t0 < t1) {
-        q0 = std::min(q0, q);
-        q1 = std::max(q1, q);
-      }
-    }
-    p.unit[x].q0 = static_cast<int16_t>(q0);
-    p.unit[x].q1 = static_cast<int16_t>(q1);
+    while (p.cut[q + 1].unit < x || (p.cut[q + 1].unit == x && p.cut[q + 1].tile == 0)) ++q;
+    p.unit[x].q0 = static_cast<int16_t>(q);
+    while (p.cut[q + 1].unit == x) ++q;  // (group q ends within x, so q + 1 goes on with it)
+    p.unit[x].q1 = static_cast<int16_t>(q);
+    const bool cut = p.unit[x].q1 > p.unit[x].q0;
     const int nodes = p.n_draft[p.unit[x].b] - p.unit[x].rb * 2 * kTrNodes;
-    p.unit[x].dup = q1 == q0 || nodes > kTrNodes / 2 ? 1 : 2;
-    if (q1 > q0) p.split = 1;
+    p.unit[x].dup = cut && nodes <= kTrNodes / 2 ? 2 : 1;
+    p.split |= cut;
   }
 }
 

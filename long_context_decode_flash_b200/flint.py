@@ -10,6 +10,7 @@ import ctypes
 import math
 import os
 import threading
+from array import array
 from typing import Optional, Sequence
 
 import torch
@@ -364,13 +365,32 @@ def _need(cond: bool, what: str) -> None:
         raise FlintError(FLINT_ERR_INVALID_ARG, what)
 
 
-def _dense(t, dtype, shape, name: str) -> None:
-    """A dense tensor of this type and shape on the current device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+def _dense(t, dtype, shape, name: str, dev: int) -> int:
+    """The address of a dense tensor of this type and shape on the CUDA device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be a dense {dtype} tensor {list(shape)}, "
                          f"not {t.dtype} {list(t.shape)}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _error_word(dev_err, dev: int) -> Optional[int]:
+    """The address of dev_err (int32, at least one value), or None."""
+    if dev_err is None:
+        return None
+    _need(dev_err.dtype is torch.int32 and dev_err.numel() > 0, "dev_err must be an int32 tensor")
+    return _dense(dev_err, torch.int32, dev_err.shape, "dev_err", dev)
+
+
+def _stream_of(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _host_i32(values: Sequence[int], n: int, name: str) -> array:
+    """Host int32 values; .buffer_info()[0] is their address."""
+    _need(len(values) == n, f"{name} must hold {n} values")
+    return array("i", values)
 
 
 def rope(rotary_dim: int = HEAD_DIM, interleaved: bool = False, theta: float = 10000.0, scaling: str = "none",
@@ -388,10 +408,9 @@ def rope(rotary_dim: int = HEAD_DIM, interleaved: bool = False, theta: float = 1
                 ROPE_INTERLEAVED if interleaved else ROPE_HALF, kinds[scaling], 0)
 
 
-def _token_rows(t, heads: int, T: int, name: str) -> int:
+def _token_rows(t, heads: int, T: int, name: str, dev: int) -> int:
     """The token stride (elements) of bf16 [T, heads, 128] with dense heads."""
-    if (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, HEAD_DIM) or t.device.type != "cuda"
-            or t.device.index != torch.cuda.current_device()):
+    if t.dtype is not torch.bfloat16 or t.shape != (T, heads, HEAD_DIM) or t.get_device() != dev:
         raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be bf16 [{T}, {heads}, 128] on the current CUDA device")
     st = t.stride()
     _need(T == 0 or st[2] == 1 and st[1] == HEAD_DIM and (T == 1 or st[0] >= heads * HEAD_DIM),
@@ -404,21 +423,23 @@ def flint_qk_norm_rope_at(q_raw, k_raw, w_q, w_k, pos, rope: Optional[Rope] = No
     """RMSNorm (unless w_q and w_k are None) and rotary positions of T tokens at
     the positions pos (device int32 [T]): q_raw [T, 32, 128] and k_raw
     [T, 4, 128] in bf16, dense or slices of wider token rows, to the dense
-    q_out and k_out."""
-    T = int(pos.shape[0])
-    _dense(pos, torch.int32, (T,), "pos")
-    qs = _token_rows(q_raw, NUM_Q_HEADS, T, "q_raw") if q_out is not None else 0
-    ks = _token_rows(k_raw, NUM_KV_HEADS, T, "k_raw") if k_out is not None else 0
+    q_out and k_out.  An input without its output is not read, and may be None."""
+    T, dev, bf16 = int(pos.shape[0]), torch.cuda.current_device(), torch.bfloat16
+    at_pos = _dense(pos, torch.int32, (T,), "pos", dev)
+    qi = ki = qo = ko = wq = wk = None
+    qs = ks = 0
     if q_out is not None:
-        _dense(q_out, torch.bfloat16, (T, NUM_Q_HEADS, HEAD_DIM), "q_out")
+        qs, qi = _token_rows(q_raw, NUM_Q_HEADS, T, "q_raw", dev), q_raw.data_ptr()
+        qo = _dense(q_out, bf16, (T, NUM_Q_HEADS, HEAD_DIM), "q_out", dev)
     if k_out is not None:
-        _dense(k_out, torch.bfloat16, (T, NUM_KV_HEADS, HEAD_DIM), "k_out")
-    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
-        if w is not None:
-            _dense(w, torch.bfloat16, (HEAD_DIM,), name)
-    _check(load_library().flint_qk_norm_rope_at(
-        _ptr(q_raw), qs, _ptr(k_raw), ks, _ptr(w_q), _ptr(w_k), _ptr(pos), T, eps,
-        ctypes.byref(rope) if rope is not None else None, _ptr(q_out), _ptr(k_out), _stream(stream)))
+        ks, ki = _token_rows(k_raw, NUM_KV_HEADS, T, "k_raw", dev), k_raw.data_ptr()
+        ko = _dense(k_out, bf16, (T, NUM_KV_HEADS, HEAD_DIM), "k_out", dev)
+    if w_q is not None:
+        wq = _dense(w_q, bf16, (HEAD_DIM,), "w_q", dev)
+    if w_k is not None:
+        wk = _dense(w_k, bf16, (HEAD_DIM,), "w_k", dev)
+    _check(load_library().flint_qk_norm_rope_at(qi, qs, ki, ks, wq, wk, at_pos, T, eps, None if rope is None else ctypes.byref(rope),
+                                                qo, ko, _stream_of(stream, dev)))
     return q_out, k_out
 
 
@@ -439,25 +460,22 @@ def flint_attn_tree(q, k_draft, v_draft, parent, cache: KVCache, seq_lens: Seque
     out bf16 [B, N, 32, 128], k_draft and v_draft bf16 [B, N, 4, 128], parent
     int32 [B, N]; seq_lens and n_draft are host values per request."""
     _need(q.dim() == 4, "q must be [B, N, 32, 128]")
-    B, N = int(q.shape[0]), int(q.shape[1])
-    _dense(q, torch.bfloat16, (B, N, NUM_Q_HEADS, HEAD_DIM), "q")
-    _dense(k_draft, torch.bfloat16, (B, N, NUM_KV_HEADS, HEAD_DIM), "k_draft")
-    _dense(v_draft, torch.bfloat16, (B, N, NUM_KV_HEADS, HEAD_DIM), "v_draft")
-    _dense(parent, torch.int32, (B, N), "parent")
-    _dense(sinks, torch.float32, (NUM_Q_HEADS,), "sinks")
-    _dense(out, torch.bfloat16, (B, N, NUM_Q_HEADS, HEAD_DIM), "out")
-    _need(len(seq_lens) == B and len(n_draft) == B, f"seq_lens and n_draft must hold {B} values")
+    B, N = q.shape[0], q.shape[1]
+    dev, bf16, heads, kv = torch.cuda.current_device(), torch.bfloat16, (B, N, NUM_Q_HEADS, HEAD_DIM), (B, N, NUM_KV_HEADS, HEAD_DIM)
+    lens, counts = _host_i32(seq_lens, B, "seq_lens"), _host_i32(n_draft, B, "n_draft")
+    _need(ws.is_contiguous() and ws.get_device() == dev, "ws must be a dense tensor on the current CUDA device")
     _check(load_library().flint_attn_tree(
-        _ptr(q), _ptr(k_draft), _ptr(v_draft), _ptr(parent), N, ctypes.byref(cache), _i32_host(seq_lens),
-        _i32_host(n_draft), B, _ptr(sinks), int(window), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
-        int(num_ctas), _ptr(dev_err), _stream(stream)))
+        _dense(q, bf16, heads, "q", dev), _dense(k_draft, bf16, kv, "k_draft", dev), _dense(v_draft, bf16, kv, "v_draft", dev),
+        _dense(parent, torch.int32, (B, N), "parent", dev), N, ctypes.byref(cache), lens.buffer_info()[0],
+        counts.buffer_info()[0], B, _dense(sinks, torch.float32, (NUM_Q_HEADS,), "sinks", dev), int(window),
+        _dense(out, bf16, heads, "out", dev), ws.data_ptr(), ws.nbytes, int(num_ctas), _error_word(dev_err, dev),
+        _stream_of(stream, dev)))
     return out
 
 
-def _prob_rows(t, B: int, rows: int, name: str) -> int:
+def _prob_rows(t, B: int, rows: int, name: str, dev: int) -> int:
     """The row stride (elements) of fp32 [B, rows, V] whose rows are evenly spaced."""
-    if (t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != rows or t.device.type != "cuda"
-            or t.device.index != torch.cuda.current_device()):
+    if t.dtype is not torch.float32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != rows or t.get_device() != dev:
         raise FlintError(FLINT_ERR_INVALID_ARG, f"{name} must be fp32 [{B}, {rows}, V] on the current CUDA device")
     b, r, v = t.stride()
     if rows == 1:
@@ -474,22 +492,22 @@ def flint_verify_tree(target, draft, tokens, parent, n_draft: Sequence[int], u_a
     the uniforms u_accept [B, N] and u_sample [B]; draft fp32 [B, N, V] holds the
     distributions that the children of each row's node were drawn from, None:
     fixed candidates.  Writes path int32 [B, N], n_accepted and next_token int32 [B]."""
-    B, N = int(tokens.shape[0]), int(tokens.shape[1])
-    ts = _prob_rows(target, B, N + 1, "target")
-    V = int(target.shape[2])
-    ds = 0
+    _need(tokens.dim() == 2, "tokens must be [B, N]")
+    B, N = tokens.shape
+    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
+    ts = _prob_rows(target, B, N + 1, "target", dev)
+    V = target.shape[2]
+    ds, at_draft = 0, None
     if draft is not None:
-        ds = _prob_rows(draft, B, N, "draft")
-        _need(int(draft.shape[2]) == V, "target and draft must have rows of one length")
-    for t, dtype, shape, name in ((tokens, torch.int32, (B, N), "tokens"), (parent, torch.int32, (B, N), "parent"),
-                                  (u_accept, torch.float32, (B, N), "u_accept"), (u_sample, torch.float32, (B,), "u_sample"),
-                                  (path, torch.int32, (B, N), "path"), (n_accepted, torch.int32, (B,), "n_accepted"),
-                                  (next_token, torch.int32, (B,), "next_token")):
-        _dense(t, dtype, shape, name)
-    _need(len(n_draft) == B, f"n_draft must hold {B} values")
+        ds, at_draft = _prob_rows(draft, B, N, "draft", dev), draft.data_ptr()
+        _need(draft.shape[2] == V, "target and draft must have rows of one length")
+    counts = _host_i32(n_draft, B, "n_draft")
     _check(load_library().flint_verify_tree(
-        _ptr(target), ts, _ptr(draft), ds, _ptr(tokens), _ptr(parent), _i32_host(n_draft), B, N, V, _ptr(u_accept),
-        _ptr(u_sample), _ptr(path), _ptr(n_accepted), _ptr(next_token), _ptr(dev_err), _stream(stream)))
+        target.data_ptr(), ts, at_draft, ds, _dense(tokens, i32, (B, N), "tokens", dev), _dense(parent, i32, (B, N), "parent", dev),
+        counts.buffer_info()[0], B, N, V, _dense(u_accept, f32, (B, N), "u_accept", dev),
+        _dense(u_sample, f32, (B,), "u_sample", dev), _dense(path, i32, (B, N), "path", dev),
+        _dense(n_accepted, i32, (B,), "n_accepted", dev), _dense(next_token, i32, (B,), "next_token", dev),
+        _error_word(dev_err, dev), _stream_of(stream, dev)))
     return path, n_accepted, next_token
 
 
@@ -497,13 +515,14 @@ def path_layers(layers) -> ctypes.Array:
     """A flint_path_layer array from (k_draft, v_draft, cache) per layer: bf16
     [B, N, 4, 128] tensors and the layer's KVCache."""
     arr = (PathLayer * len(layers))()
-    shape = tuple(layers[0][0].shape) if len(layers) else ()
+    shape, dev = tuple(layers[0][0].shape) if len(layers) else (), torch.cuda.current_device()
     for i, (k, v, cache) in enumerate(layers):
-        for t, name in ((k, "k"), (v, "v")):
-            _need(len(shape) == 4, "the drafts must be [B, N, 4, 128]")
-            _dense(t, torch.bfloat16, shape[:2] + (NUM_KV_HEADS, HEAD_DIM), f"layer {i}: {name}")
-        arr[i].k, arr[i].v, arr[i].cache = k.data_ptr(), v.data_ptr(), cache
-    arr._keep, arr._shape = list(layers), shape[:2]
+        _need(len(shape) == 4, "the drafts must be [B, N, 4, 128]")
+        full = shape[:2] + (NUM_KV_HEADS, HEAD_DIM)
+        arr[i].k = _dense(k, torch.bfloat16, full, f"layer {i}: k", dev)
+        arr[i].v = _dense(v, torch.bfloat16, full, f"layer {i}: v", dev)
+        arr[i].cache = cache
+    arr._keep, arr._shape, arr._dev = list(layers), shape[:2], dev
     return arr
 
 
@@ -511,14 +530,14 @@ def flint_kv_append_path(layers, path, n_accepted, seq_lens: Sequence[int], dev_
     """Append the drafted k and v of the accepted nodes path[b, :n_accepted[b]]
     (device int32) at positions seq_lens[b] .. of every layer's cache; layers:
     an array from path_layers() or a list for it."""
-    arr = layers if isinstance(layers, ctypes.Array) else path_layers(layers)
-    _need(len(arr) > 0 and path.dim() == 2 and tuple(path.shape) == arr._shape, "path must be [B, N] as the layers' drafts are")
-    B, N = int(path.shape[0]), int(path.shape[1])
-    _dense(path, torch.int32, (B, N), "path")
-    _dense(n_accepted, torch.int32, (B,), "n_accepted")
-    _need(len(seq_lens) == B, f"seq_lens must hold {B} values")
-    _check(load_library().flint_kv_append_path(arr, len(arr), _ptr(path), _ptr(n_accepted), N, _i32_host(seq_lens), B,
-                                               _ptr(dev_err), _stream(stream)))
+    arr, dev = layers if isinstance(layers, ctypes.Array) else path_layers(layers), torch.cuda.current_device()
+    _need(len(arr) > 0 and path.shape == arr._shape, "path must be [B, N] as the layers' drafts are")
+    _need(arr._dev == dev, "the layers are not on the current CUDA device")
+    B, N = path.shape
+    lens = _host_i32(seq_lens, B, "seq_lens")
+    _check(load_library().flint_kv_append_path(
+        arr, len(arr), _dense(path, torch.int32, (B, N), "path", dev), _dense(n_accepted, torch.int32, (B,), "n_accepted", dev), N,
+        lens.buffer_info()[0], B, _error_word(dev_err, dev), _stream_of(stream, dev)))
 
 
 def flint_plan_items(seg_tiles: Sequence[int], num_ctas: int, item_cost: int = 2,
