@@ -5,9 +5,8 @@
 // full batch over all layers, by HBM: each accepted token's 2 KiB is read and
 // written once per layer.
 //
-// One CTA per (request, layer); warps take the path's tokens in turn, four warps
-// to a token (k and v of 512 values, 8 a lane), so that the tokens of a path are
-// in flight together.
+// One CTA per (token of a path, request, up to 7 layers): 64 threads for k and 64
+// for v, 8 values each, with the loads of all its layers in flight together.
 #include <algorithm>
 
 #include "flint_device.cuh"
@@ -17,64 +16,92 @@ namespace flint {
 
 namespace {
 
-constexpr int kApTokens = 2;               // tokens a CTA has in flight
-constexpr int kApThreads = 128 * kApTokens;
+constexpr int kApLayers = 7;               // layers a CTA has in flight, at most
 
-// The code of x / s, the quotient a float32 rounded to nearest.  q0 = x r with r
-// = 1 / s rounded is within 2^-23 of the quotient, two units in the last place;
-// codes change only at numbers of 5 significant bits (midpoints of codes), so
-// unless q0 is within 3 units of such a number the quotient itself has q0's code.
-// There, and where 1 / s may not be a normal number (r = 0), the division decides.
-__device__ __forceinline__ float quotient_for_code(float x, float s, float r) {
-  const float q0 = x * r;
-  if (((__float_as_uint(q0) + 3u) & 0x7FFFFu) > 6u) return q0;
-  return __fdiv_rn(x, s);
+// The codes of 8 values over s, each quotient a float32 rounded to nearest.  q = x
+// r with r = 1 / s rounded is within 2^-23 of the quotient, two units in the last
+// place; codes change only at numbers of 5 significant bits (midpoints of codes),
+// so unless q is within 3 units of such a number the quotient itself has q's code.
+// Where one of the 8 is, or 1 / s may not be a normal number (r = 0), division
+// decides.
+__device__ __forceinline__ uint2 codes_of(uint4 x, float s, float r) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t code[4], far = 0x7FFFFu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = bf16_lo(w[i]) * r, b = bf16_hi(w[i]) * r;
+    far = min(far, min((__float_as_uint(a) + 3u) & 0x7FFFFu, (__float_as_uint(b) + 3u) & 0x7FFFFu));
+    code[i] = f32x2_to_e4m3x2(a, b);
+  }
+  if (far <= 6u) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+      const uint32_t z = f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(y), s), __fdiv_rn(bf16_hi(y), s));
+      if (i == 0) code[0] = z;
+      else if (i == 1) code[1] = z;
+      else if (i == 2) code[2] = z;
+      else code[3] = z;
+    }
+  }
+  return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
 }
 
-__global__ void __launch_bounds__(kApThreads) append_path_kernel(const __grid_constant__ AppendPathParams p) {
-  const int b = blockIdx.x;
-  const PathLayer& ly = p.layer[blockIdx.y];
-  const int c = threadIdx.x & 63;  // 8-dim chunk of the token's 512 values
-  const bool is_v = threadIdx.x & 64;
-  const int n = p.n_accepted[b];
+__global__ void __launch_bounds__(128) append_path_kernel(const __grid_constant__ AppendPathParams p, int layers) {
+  const int b = blockIdx.y, j = blockIdx.x, l0 = blockIdx.z * layers, nl = min(layers, p.n_layers - l0);
+  const int n = p.n_accepted[b], node = p.path[static_cast<long long>(b) * p.N + j], pos = p.len[b] + j;
   if (n < 0 || n > p.N) {
     if (threadIdx.x == 0) report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
     return;
   }
-  const float s = is_v ? ly.v_scale[c / 16] : ly.k_scale[c / 16];
-  const float r = s > 1e-30f && s < 1e30f ? 1.0f / s : 0.f;
-  for (int j = threadIdx.x / 128; j < n; j += kApTokens) {
-    const int node = p.path[static_cast<long long>(b) * p.N + j], pos = p.len[b] + j;
+  if (j >= n) return;
+  const int c = threadIdx.x & 63;  // 8-dim chunk of the token's 512 values
+  const bool is_v = threadIdx.x & 64;
+  const bool exists = node >= 0 && node < p.N;
+  const long long from = (static_cast<long long>(b) * p.N + node) * kKvHeads * kDim;
+  uint4 x[kApLayers];
+  int blk[kApLayers];
+#pragma unroll
+  for (int k = 0; k < kApLayers; ++k) {
+    if (k >= nl) continue;
+    const PathLayer& ly = p.layer[l0 + k];
+    if (exists) x[k] = reinterpret_cast<const uint4*>((is_v ? ly.v : ly.k) + from)[c];
+    blk[k] = -1;
+    if (ly.layout == FLINT_KV_PAGED && pos / kBlock < ly.max_blocks) blk[k] = ly.table[static_cast<long long>(b) * ly.max_blocks + pos / kBlock];
+  }
+#pragma unroll
+  for (int k = 0; k < kApLayers; ++k) {
+    if (k >= nl) continue;
+    const PathLayer& ly = p.layer[l0 + k];
     long long row = -1;  // element offset of the slot
-    if (node >= 0 && node < p.N) {
+    if (exists) {
       if (ly.layout == FLINT_KV_PAGED) {
-        if (pos / kBlock < ly.max_blocks) {
-          const int blk = ly.table[static_cast<long long>(b) * ly.max_blocks + pos / kBlock];
-          if (blk >= 0 && blk < ly.num_blocks) row = (static_cast<long long>(blk) * kBlock + pos % kBlock) * kKvHeads * kDim;
-        }
+        if (blk[k] >= 0 && blk[k] < ly.num_blocks) row = (static_cast<long long>(blk[k]) * kBlock + pos % kBlock) * kKvHeads * kDim;
       } else if (ly.layout == FLINT_KV_RING || pos < ly.capacity) {
         row = b * ly.req_stride + static_cast<long long>(pos % ly.capacity) * kKvHeads * kDim;
       }
     }
     if (row < 0) {
-      if (c == 0) report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
+      if (threadIdx.x == 0) report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
       continue;
     }
-    const uint4 x = reinterpret_cast<const uint4*>((is_v ? ly.v : ly.k) + (static_cast<long long>(b) * p.N + node) * kKvHeads * kDim)[c];
     uint8_t* dst = is_v ? ly.v_rows : ly.k_rows;
     if (!ly.fp8) {
-      *reinterpret_cast<uint4*>(dst + 2 * (row + 8 * c)) = x;
+      *reinterpret_cast<uint4*>(dst + 2 * (row + 8 * c)) = x[k];
     } else {
-      auto two = [&](uint32_t w) { return f32x2_to_e4m3x2(quotient_for_code(bf16_lo(w), s, r), quotient_for_code(bf16_hi(w), s, r)); };
-      *reinterpret_cast<uint2*>(dst + row + 8 * c) = make_uint2(two(x.x) | two(x.y) << 16, two(x.z) | two(x.w) << 16);
+      const float s = is_v ? ly.v_scale[c / 16] : ly.k_scale[c / 16];
+      *reinterpret_cast<uint2*>(dst + row + 8 * c) = codes_of(x[k], s, s > 1e-30f && s < 1e30f ? 1.0f / s : 0.f);
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_append_path(const AppendPathParams& p, cudaStream_t stream) {
-  append_path_kernel<<<dim3(p.B, p.n_layers), kApThreads, 0, stream>>>(p);
+cudaError_t launch_append_path(const AppendPathParams& p, int num_sms, cudaStream_t stream) {
+  // as many layers a CTA as leave a full set of CTAs (16 a SM)
+  const long long jobs = static_cast<long long>(p.B) * p.N * p.n_layers;
+  const int layers = static_cast<int>(std::min<long long>(kApLayers, std::max<long long>(1, jobs / (16ll * num_sms))));
+  append_path_kernel<<<dim3(p.N, p.B, (p.n_layers + layers - 1) / layers), 128, 0, stream>>>(p, layers);
   return cudaGetLastError();
 }
 

@@ -22,6 +22,7 @@ namespace flint {
 namespace {
 
 constexpr int kRaWarps = 8, kRaThreads = kRaWarps * 32;
+constexpr int kAhead = 3;
 constexpr int kPairsOfRows = (kHeads + kKvHeads) / 2;  // 18: 16 of q, 2 of k
 
 enum { kInLane, kByLanes, kByShared };
@@ -37,23 +38,30 @@ __global__ void __launch_bounds__(kRaThreads) rope_at_kernel(const __grid_consta
   const int half = p.rotary_dim / 2, d0 = 8 * c;  // this lane's dims d0 .. d0 + 7
   if (threadIdx.x < half) turns[threadIdx.x] = p.turns[threadIdx.x];
   __syncthreads();
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (p.w_q) {
+    wq = reinterpret_cast<const uint4*>(p.w_q)[c];
+    wk = reinterpret_cast<const uint4*>(p.w_k)[c];
+  }
   const long long jobs = static_cast<long long>(p.T) * parts;
 #pragma unroll 1
   for (long long job = static_cast<long long>(blockIdx.x) * kRaWarps + warp; job < jobs; job += static_cast<long long>(gridDim.x) * kRaWarps) {
     const long long t = job / parts;
     const int part = static_cast<int>(job % parts);
-    // rows part * 2 + (lane >> 4), ...: q rows first
-    constexpr int kAhead = 3;
-    auto want = [&](int pair) { return pair < kPairsOfRows && (pair < kHeads / 2 ? p.q_out : p.k_out) != nullptr; };
+    // rows 2 * pair + (lane >> 4), q's first; the next kAhead pairs are in flight
     auto load = [&](int pair) {
+      uint4 x = make_uint4(0, 0, 0, 0);
       const int r = 2 * pair + (lane >> 4);
-      const uint16_t* x = r < kHeads ? p.q_raw + t * p.q_stride + r * kDim : p.k_raw + t * p.k_stride + (r - kHeads) * kDim;
-      return reinterpret_cast<const uint4*>(x)[c];
+      if (pair < kHeads / 2) {
+        if (p.q_out) x = reinterpret_cast<const uint4*>(p.q_raw + t * p.q_stride + r * kDim)[c];
+      } else if (pair < kPairsOfRows && p.k_out) {
+        x = reinterpret_cast<const uint4*>(p.k_raw + t * p.k_stride + (r - kHeads) * kDim)[c];
+      }
+      return x;
     };
-    uint4 next[kAhead];
+    uint4 ahead[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (want(part + i * parts)) next[i] = load(part + i * parts);
+    for (int i = 0; i < kAhead; ++i) ahead[i] = load(part + i * parts);
     // cos and sin of the token's pairs
     const int pos = p.pos[t];
     __syncwarp();
@@ -64,86 +72,83 @@ __global__ void __launch_bounds__(kRaThreads) rope_at_kernel(const __grid_consta
       cs[warp][i] = make_float2(co * p.attn_factor, s * p.attn_factor);
     }
     __syncwarp();
-#pragma unroll 1
-    for (int pair0 = part; pair0 < kPairsOfRows; pair0 += kAhead * parts) {
-      uint4 now[kAhead];
+    // a value's own: y cos + (its partner) sin, sin negative for the first of a pair
+    constexpr int kCs = kAt == kInLane ? 4 : 8;
+    float2 mine[kCs];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) now[i] = next[i];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (want(pair0 + (kAhead + i) * parts)) next[i] = load(pair0 + (kAhead + i) * parts);
+    for (int e = 0; e < kCs; ++e) {
+      if (kAt == kInLane) {
+        mine[e] = d0 / 2 + e < half ? cs[warp][d0 / 2 + e] : make_float2(1.f, 0.f);
+      } else {
+        const int d = d0 + e;
+        const bool second = d >= half;
+        mine[e] = d < 2 * half ? cs[warp][second ? d - half : d] : make_float2(1.f, 0.f);
+        if (!second) mine[e].y = -mine[e].y;
+      }
+    }
 #pragma unroll 1
-      for (int i = 0; i < kAhead; ++i) {
-        const int pair = pair0 + i * parts;
-        if (!want(pair)) continue;
-        const int r = 2 * pair + (lane >> 4);
-        const uint4 raw = i == 0 ? now[0] : i == 1 ? now[1] : now[2];
-        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-        float y[8];
+    for (int pair = part; pair < kPairsOfRows; pair += parts) {
+      const uint4 raw = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      ahead[kAhead - 1] = load(pair + kAhead * parts);
+      const bool is_q = pair < kHeads / 2;
+      uint16_t* o = is_q ? p.q_out : p.k_out;
+      if (!o) continue;
+      const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[2 * e] = bf16_lo(x[e]);
+        y[2 * e + 1] = bf16_hi(x[e]);
+      }
+      if (p.w_q) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+        const float inv = rsqrtf(fmaf(ss, 1.0f / kDim, p.eps));
+        const uint4 wr = is_q ? wq : wk;
+        const uint32_t wx[4] = {wr.x, wr.y, wr.z, wr.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[2 * e] = bf16_lo(x[e]);
-          y[2 * e + 1] = bf16_hi(x[e]);
+          y[2 * e] = y[2 * e] * inv * bf16_lo(wx[e]);
+          y[2 * e + 1] = y[2 * e + 1] * inv * bf16_hi(wx[e]);
         }
-        const uint16_t* w = r < kHeads ? p.w_q : p.w_k;
-        if (w) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
-#pragma unroll
-          for (int k = 8; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
-          const float inv = 1.0f / sqrtf(ss * (1.0f / kDim) + p.eps);
-          const uint4 wr = reinterpret_cast<const uint4*>(w)[c];
-          const uint32_t wx[4] = {wr.x, wr.y, wr.z, wr.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] = y[2 * e] * inv * bf16_lo(wx[e]);
-            y[2 * e + 1] = y[2 * e + 1] * inv * bf16_hi(wx[e]);
-          }
-        }
-        if (kAt == kInLane) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int j = (d0 + e) >> 1;
-            if (j < half) {
-              const float2 a = cs[warp][j];
-              const float u = y[e], v = y[e + 1];
-              y[e] = u * a.x - v * a.y;
-              y[e + 1] = v * a.x + u * a.y;
-            }
-          }
-        } else if (kAt == kByLanes) {  // half is a multiple of 8: whole lanes pair up
-          const bool turned = d0 < 2 * half, second = d0 >= half;
-          const int other = turned ? (second ? lane - half / 8 : lane + half / 8) : lane;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = __shfl_sync(0xffffffffu, y[e], other);
-            if (turned) {
-              const float2 a = cs[warp][(second ? d0 - half : d0) + e];
-              y[e] = second ? y[e] * a.x + z * a.y : y[e] * a.x - z * a.y;
-            }
-          }
-        } else {
-          float* mine = rows[warp] + (lane >> 4) * kDim;
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mine[d0 + e] = y[e];
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e;
-            if (d < 2 * half) {
-              const bool second = d >= half;
-              const float2 a = cs[warp][second ? d - half : d];
-              const float z = mine[second ? d - half : d + half];
-              y[e] = second ? y[e] * a.x + z * a.y : y[e] * a.x - z * a.y;
-            }
-          }
-        }
-        uint16_t* o = r < kHeads ? p.q_out + (t * kHeads + r) * kDim : p.k_out + (t * kKvHeads + r - kHeads) * kDim;
-        reinterpret_cast<uint4*>(o)[c] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                                    pack_bf16x2(y[6], y[7]));
       }
+      if (kAt == kInLane) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (d0 / 2 + e < half) {
+            const float u = y[2 * e], v = y[2 * e + 1];
+            y[2 * e] = u * mine[e].x - v * mine[e].y;
+            y[2 * e + 1] = v * mine[e].x + u * mine[e].y;
+          }
+      } else if (kAt == kByLanes) {  // half is a multiple of 8: whole lanes pair up
+        const bool turned = d0 < 2 * half;
+        const int other = turned ? (d0 >= half ? lane - half / 8 : lane + half / 8) : lane;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float z = __shfl_sync(0xffffffffu, y[e], other);
+          if (turned) y[e] = y[e] * mine[e].x + z * mine[e].y;
+        }
+      } else {
+        float* row = rows[warp] + (lane >> 4) * kDim;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) row[d0 + e] = y[e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = d0 + e;
+          if (d < 2 * half) y[e] = y[e] * mine[e].x + row[d >= half ? d - half : d + half] * mine[e].y;
+        }
+      }
+      const int r = 2 * pair + (lane >> 4);
+      o += is_q ? (t * kHeads + r) * kDim : (t * kKvHeads + r - kHeads) * kDim;
+      reinterpret_cast<uint4*>(o)[c] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                                  pack_bf16x2(y[6], y[7]));
     }
   }
 }

@@ -48,7 +48,7 @@ struct AppendPathParams {
   int32_t n_layers, N, B;
 };
 static_assert(sizeof(AppendPathParams) <= 32000, "kernel parameters exceed 32 KiB");
-cudaError_t launch_append_path(const AppendPathParams& p, cudaStream_t stream);
+cudaError_t launch_append_path(const AppendPathParams& p, int num_sms, cudaStream_t stream);
 
 // ---- flint_verify_tree ------------------------------------------------------------
 struct VerifyParams {

@@ -319,7 +319,9 @@ flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_laye
   p.n_layers = n_layers;
   p.N = N;
   p.B = B;
-  return launched(launch_append_path(p, static_cast<cudaStream_t>(stream)), who);
+  int sms = 0;
+  if (device_num_sms(&sms) != 0) return record_error(FLINT_ERR_CUDA, "%s: cannot read the device's SM count", who);
+  return launched(launch_append_path(p, sms, static_cast<cudaStream_t>(stream)), who);
 }
 
 }  // extern "C"

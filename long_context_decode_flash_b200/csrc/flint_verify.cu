@@ -8,7 +8,7 @@
 // never stored.  Then the next token is the first whose running sum of w
 // exceeds u sum(w).
 //
-// A cluster of CTAs per request, up to 8 so that a batch fills the SMs.  The
+// A cluster of CTAs per request, up to 16 so that a batch fills the SMs.  The
 // walk needs two numbers a node, fetched at once; only a rejection, and the
 // draw at the end, reads a row, each CTA its part.  The warps' sums over
 // contiguous shares (in double: the draw decides at borders) meet through the
@@ -29,9 +29,10 @@ namespace flint {
 
 namespace {
 
-constexpr int kVfWarps = 16, kVfThreads = kVfWarps * 32;
-constexpr int kVfCluster = 8;              // CTAs per request, at most
+constexpr int kVfWarps = 8, kVfThreads = kVfWarps * 32;
+constexpr int kVfCluster = 16;             // CTAs per request, at most
 constexpr int kVfShares = kVfCluster * kVfWarps;
+static_assert(kVfShares == 128, "four shares a lane");
 
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
@@ -53,28 +54,51 @@ struct Residual {
       if (tok[__ffsll(r) - 1] == y) return 0.0;
     return t;
   }
-  // A warp's sum over [v0, v1) (16 loads in flight a lane).
-  __device__ __forceinline__ double sum(int v0, int v1, int lane) const {
+  // A warp's sum over [v0, v1): 8 loads a lane (16 with a draft) in flight while
+  // the 8 before them are summed.
+  enum { kAlone, kDraft, kOut };
+  template <int kMode>
+  __device__ __forceinline__ double sum_of(int v0, int v1, int lane) const {
     double s0 = 0.0, s1 = 0.0;
-    for (int y = v0 + lane; y < v1; y += 8 * 32) {
-      float t[8], d[8];
+    float t[8], d[8];
+    auto load = [&](int y) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int z = y + 32 * k;
         t[k] = z < v1 ? target[z] : 0.f;
-        d[k] = draft && z < v1 ? draft[z] : 0.f;
+        if (kMode == kDraft) d[k] = z < v1 ? draft[z] : 0.f;
       }
+    };
+    load(v0 + lane);
+    for (int y = v0 + lane; y < v1; y += 8 * 32) {
+      float a[8], e[8];
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) {
-        s0 += of(y + 32 * k, t[k], d[k]);
-        s1 += of(y + 32 * k + 32, t[k + 1], d[k + 1]);
+      for (int k = 0; k < 8; ++k) {
+        a[k] = t[k];
+        e[k] = kMode == kDraft ? d[k] : 0.f;
+      }
+      load(y + 8 * 32);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const double x = kMode == kAlone ? static_cast<double>(a[k]) : of(y + 32 * k, a[k], e[k]);
+        if (k & 1) s1 += x;
+        else s0 += x;
       }
     }
     return warp_sum(s0 + s1);
   }
+  __device__ __forceinline__ double sum(int v0, int v1, int lane) const {
+    if (draft) return sum_of<kDraft>(v0, v1, lane);
+    bool here = false;  // a candidate that was taken out lies in the range
+    for (unsigned long long r = out; r; r &= r - 1) {
+      const int x = tok[__ffsll(r) - 1];
+      here |= x >= v0 && x < v1;
+    }
+    return here ? sum_of<kOut>(v0, v1, lane) : sum_of<kAlone>(v0, v1, lane);
+  }
 };
 
-__global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ double pt[kMaxTree], pd[kMaxTree];  // target and draft probability of node i's token at its parent
   __shared__ double mine[2][kVfWarps];           // this CTA's shares' sums (by pass parity: others read them)
   __shared__ double all[kVfShares], below[kVfShares];  // every share's sum, and the sum of those before it
@@ -150,8 +174,17 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
     ++pass;
   };
   bool summed = false;  // all[], below[] and total are w's
-  for (int i = 0; i < n; ++i) {
-    if (par[i] != cur || tok[i] < 0) continue;
+  // the nodes behind node i whose parent is `node`, as bits
+  auto children = [&](int node, int i) {
+    const int a = lane, e = lane + 32;
+    const unsigned lo = __ballot_sync(0xffffffffu, a < n && par[a] == node && tok[a] >= 0);
+    const unsigned hi = __ballot_sync(0xffffffffu, e < n && par[e] == node && tok[e] >= 0);
+    const unsigned long long all_of = static_cast<unsigned long long>(hi) << 32 | lo;
+    return i < 0 ? all_of : i >= 63 ? 0ull : all_of & (~0ull << (i + 1));
+  };
+  for (unsigned long long left = children(-1, -1); left;) {
+    const int i = __ffsll(left) - 1;
+    left &= left - 1;
     const double wx = draft ? fmax(__dsub_rn(pt[i], __dmul_rn(w.c, pd[i])), 0.0) : w.of(tok[i], static_cast<float>(pt[i]), 0.f);
     if (u[i] * pd[i] * Z < wx) {
       if (rank == 0 && threadIdx.x == 0) p.path[static_cast<long long>(b) * p.N + taken] = i;
@@ -160,6 +193,7 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
       w = Residual{target + (cur + 1) * p.target_stride, nullptr, 0.0, tok, 0};
       Z = 1.0;
       summed = false;
+      left = children(cur, i);
     } else if (draft) {
       Residual r = w;
       r.draft = draft + (cur + 1) * p.draft_stride;
@@ -254,9 +288,19 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& p, int num_sms, cudaStream_t stream) {
-  // CTAs per request: up to two a SM over the batch, at least 512 values each
+  // CTAs per request: up to four a SM over the batch, at least 512 values each
   int C = 1;
-  while (C < kVfCluster && 2 * C * p.B <= 2 * num_sms && p.V / (2 * C) >= kVfThreads) C *= 2;
+  while (C < kVfCluster && 2 * C * p.B <= 4 * num_sms && p.V / (2 * C) >= 2 * kVfThreads) C *= 2;
+  if (C > 8) {  // a cluster beyond the portable size
+    static ContextSet configured;
+    void* ctx = current_context();
+    std::lock_guard<std::mutex> lock(configured.mu);
+    if (!ctx || std::find(configured.ctxs.begin(), configured.ctxs.end(), ctx) == configured.ctxs.end()) {
+      const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (ctx) configured.ctxs.push_back(ctx);
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C * p.B);
   cfg.blockDim = dim3(kVfThreads);
