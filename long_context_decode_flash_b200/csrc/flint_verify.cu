@@ -56,45 +56,62 @@ struct Residual {
   }
   // A warp's sum over [v0, v1): 8 loads a lane (16 with a draft) in flight while
   // the 8 before them are summed.
-  enum { kAlone, kDraft, kOut };
-  template <int kMode>
+  template <bool kDraft>
   __device__ __forceinline__ double sum_of(int v0, int v1, int lane) const {
     double s0 = 0.0, s1 = 0.0;
-    float t[8], d[8];
-    auto load = [&](int y) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int z = y + 32 * k;
-        t[k] = z < v1 ? target[z] : 0.f;
-        if (kMode == kDraft) d[k] = z < v1 ? draft[z] : 0.f;
-      }
+    constexpr int kStep = 8 * 32;
+    const int full = v0 + (v1 - v0) / kStep * kStep;
+    auto add = [&](int k, float a, float e) {
+      const double x = kDraft ? fmax(__dsub_rn(a, __dmul_rn(c, e)), 0.0) : static_cast<double>(a);
+      if (k & 1) s1 += x;
+      else s0 += x;
     };
-    load(v0 + lane);
-    for (int y = v0 + lane; y < v1; y += 8 * 32) {
-      float a[8], e[8];
+    float t[8], d[8];
+    if (full > v0) {
+      auto load = [&](int y) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a[k] = t[k];
-        e[k] = kMode == kDraft ? d[k] : 0.f;
-      }
-      load(y + 8 * 32);
+        for (int k = 0; k < 8; ++k) {
+          t[k] = target[y + 32 * k];
+          if (kDraft) d[k] = draft[y + 32 * k];
+        }
+      };
+      load(v0 + lane);
+      for (int y = v0; y < full; y += kStep) {
+        float a[8], e[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const double x = kMode == kAlone ? static_cast<double>(a[k]) : of(y + 32 * k, a[k], e[k]);
-        if (k & 1) s1 += x;
-        else s0 += x;
+        for (int k = 0; k < 8; ++k) {
+          a[k] = t[k];
+          e[k] = kDraft ? d[k] : 0.f;
+        }
+        load((y + kStep < full ? y + kStep : v0) + lane);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(k, a[k], e[k]);
       }
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int z = full + lane + 32 * k;
+      t[k] = z < v1 ? target[z] : 0.f;
+      d[k] = kDraft && z < v1 ? draft[z] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add(k, t[k], d[k]);
     return warp_sum(s0 + s1);
   }
   __device__ __forceinline__ double sum(int v0, int v1, int lane) const {
-    if (draft) return sum_of<kDraft>(v0, v1, lane);
-    bool here = false;  // a candidate that was taken out lies in the range
-    for (unsigned long long r = out; r; r &= r - 1) {
-      const int x = tok[__ffsll(r) - 1];
-      here |= x >= v0 && x < v1;
+    if (draft) return sum_of<true>(v0, v1, lane);
+    // the ranges between the candidates that were taken out, in order
+    double s = 0.0;
+    for (int from = v0; from < v1;) {
+      int to = v1;
+      for (unsigned long long r = out; r; r &= r - 1) {
+        const int x = tok[__ffsll(r) - 1];
+        if (x >= from && x < to) to = x;
+      }
+      s += sum_of<false>(from, to, lane);
+      from = to + 1;
     }
-    return here ? sum_of<kOut>(v0, v1, lane) : sum_of<kAlone>(v0, v1, lane);
+    return s;
   }
 };
 
