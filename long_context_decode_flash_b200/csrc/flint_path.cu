@@ -5,8 +5,9 @@
 // full batch over all layers, by HBM: each accepted token's 2 KiB is read and
 // written once per layer.
 //
-// One CTA per (token of a path, request, up to 7 layers): 64 threads for k and 64
-// for v, 8 values each, with the loads of all its layers in flight together.
+// One CTA per (token of a path, request, up to 8 layers): two layers at a time, 32
+// threads for k and 32 for v, 16 values each, with the loads of all its layers in
+// flight together.
 #include <algorithm>
 
 #include "flint_device.cuh"
@@ -16,7 +17,8 @@ namespace flint {
 
 namespace {
 
-constexpr int kApLayers = 7;               // layers a CTA has in flight, at most
+constexpr int kApThreads = 128;
+constexpr int kApLayers = 8;               // layers a CTA has in flight, at most
 
 // The codes of 8 values over s, each quotient a float32 rounded to nearest.  q = x
 // r with r = 1 / s rounded is within 2^-23 of the quotient, two units in the last
@@ -47,7 +49,7 @@ __device__ __forceinline__ uint2 codes_of(uint4 x, float s, float r) {
   return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
 }
 
-__global__ void __launch_bounds__(128) append_path_kernel(const __grid_constant__ AppendPathParams p, int layers) {
+__global__ void __launch_bounds__(kApThreads) append_path_kernel(const __grid_constant__ AppendPathParams p, int layers) {
   const int b = blockIdx.y, j = blockIdx.x, l0 = blockIdx.z * layers, nl = min(layers, p.n_layers - l0);
   const int n = p.n_accepted[b], node = p.path[static_cast<long long>(b) * p.N + j], pos = p.len[b] + j;
   if (n < 0 || n > p.N) {
@@ -55,42 +57,50 @@ __global__ void __launch_bounds__(128) append_path_kernel(const __grid_constant_
     return;
   }
   if (j >= n) return;
-  const int c = threadIdx.x & 63;  // 8-dim chunk of the token's 512 values
-  const bool is_v = threadIdx.x & 64;
+  const int c = threadIdx.x & 31;  // 16-dim chunk of the token's 512 values
+  const bool is_v = threadIdx.x & 32;
+  const int k0 = threadIdx.x >> 6;  // layers k0, k0 + 2, ..
   const bool exists = node >= 0 && node < p.N;
   const long long from = (static_cast<long long>(b) * p.N + node) * kKvHeads * kDim;
-  uint4 x[kApLayers];
-  int blk[kApLayers];
+  uint4 x[kApLayers / 2][2];
+  int blk[kApLayers / 2];
 #pragma unroll
-  for (int k = 0; k < kApLayers; ++k) {
-    if (k >= nl) continue;
-    const PathLayer& ly = p.layer[l0 + k];
-    if (exists) x[k] = reinterpret_cast<const uint4*>((is_v ? ly.v : ly.k) + from)[c];
-    blk[k] = -1;
-    if (ly.layout == FLINT_KV_PAGED && pos / kBlock < ly.max_blocks) blk[k] = ly.table[static_cast<long long>(b) * ly.max_blocks + pos / kBlock];
+  for (int i = 0; i < kApLayers / 2; ++i) {
+    if (k0 + 2 * i >= nl) continue;
+    const PathLayer& ly = p.layer[l0 + k0 + 2 * i];
+    if (exists) {
+      const uint4* src = reinterpret_cast<const uint4*>((is_v ? ly.v : ly.k) + from) + 2 * c;
+      x[i][0] = src[0];
+      x[i][1] = src[1];
+    }
+    blk[i] = -1;
+    if (ly.layout == FLINT_KV_PAGED && pos / kBlock < ly.max_blocks) blk[i] = ly.table[static_cast<long long>(b) * ly.max_blocks + pos / kBlock];
   }
 #pragma unroll
-  for (int k = 0; k < kApLayers; ++k) {
-    if (k >= nl) continue;
-    const PathLayer& ly = p.layer[l0 + k];
+  for (int i = 0; i < kApLayers / 2; ++i) {
+    if (k0 + 2 * i >= nl) continue;
+    const PathLayer& ly = p.layer[l0 + k0 + 2 * i];
     long long row = -1;  // element offset of the slot
     if (exists) {
       if (ly.layout == FLINT_KV_PAGED) {
-        if (blk[k] >= 0 && blk[k] < ly.num_blocks) row = (static_cast<long long>(blk[k]) * kBlock + pos % kBlock) * kKvHeads * kDim;
+        if (blk[i] >= 0 && blk[i] < ly.num_blocks) row = (static_cast<long long>(blk[i]) * kBlock + pos % kBlock) * kKvHeads * kDim;
       } else if (ly.layout == FLINT_KV_RING || pos < ly.capacity) {
         row = b * ly.req_stride + static_cast<long long>(pos % ly.capacity) * kKvHeads * kDim;
       }
     }
     if (row < 0) {
-      if (threadIdx.x == 0) report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
+      if (c == 0) report_error(p.dev_err, FLINT_ERR_INVALID_ARG);
       continue;
     }
     uint8_t* dst = is_v ? ly.v_rows : ly.k_rows;
     if (!ly.fp8) {
-      *reinterpret_cast<uint4*>(dst + 2 * (row + 8 * c)) = x[k];
+      uint4* to = reinterpret_cast<uint4*>(dst + 2 * row) + 2 * c;
+      to[0] = x[i][0];
+      to[1] = x[i][1];
     } else {
-      const float s = is_v ? ly.v_scale[c / 16] : ly.k_scale[c / 16];
-      *reinterpret_cast<uint2*>(dst + row + 8 * c) = codes_of(x[k], s, s > 1e-30f && s < 1e30f ? 1.0f / s : 0.f);
+      const float s = is_v ? ly.v_scale[c / 8] : ly.k_scale[c / 8], r = is_v ? ly.v_inv[c / 8] : ly.k_inv[c / 8];
+      const uint2 a = codes_of(x[i][0], s, r), d = codes_of(x[i][1], s, r);
+      reinterpret_cast<uint4*>(dst + row)[c] = make_uint4(a.x, a.y, d.x, d.y);
     }
   }
 }
@@ -101,7 +111,7 @@ cudaError_t launch_append_path(const AppendPathParams& p, int num_sms, cudaStrea
   // as many layers a CTA as leave a full set of CTAs (16 a SM)
   const long long jobs = static_cast<long long>(p.B) * p.N * p.n_layers;
   const int layers = static_cast<int>(std::min<long long>(kApLayers, std::max<long long>(1, jobs / (16ll * num_sms))));
-  append_path_kernel<<<dim3(p.N, p.B, (p.n_layers + layers - 1) / layers), 128, 0, stream>>>(p, layers);
+  append_path_kernel<<<dim3(p.N, p.B, (p.n_layers + layers - 1) / layers), kApThreads, 0, stream>>>(p, layers);
   return cudaGetLastError();
 }
 

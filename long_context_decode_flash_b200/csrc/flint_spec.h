@@ -38,6 +38,7 @@ struct PathLayer {
   int64_t req_stride;        // elements
   int32_t layout, capacity, max_blocks, num_blocks, fp8;
   float k_scale[4], v_scale[4];
+  float k_inv[4], v_inv[4];  // 1 / scale rounded, 0 where that may not be a normal number
 };
 struct AppendPathParams {
   PathLayer layer[FLINT_MAX_LAYERS];

@@ -311,6 +311,8 @@ flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_laye
     for (int g = 0; g < kKvHeads; ++g) {
       to.k_scale[g] = c.k_scale[g];
       to.v_scale[g] = c.v_scale[g];
+      to.k_inv[g] = to.k_scale[g] > 1e-30f && to.k_scale[g] < 1e30f ? 1.0f / to.k_scale[g] : 0.f;
+      to.v_inv[g] = to.v_scale[g] > 1e-30f && to.v_scale[g] < 1e30f ? 1.0f / to.v_scale[g] : 0.f;
     }
   }
   p.path = path;
