@@ -81,12 +81,14 @@ constexpr size_t kTreeGroupBytes = size_t(kKvHeads) * 2 * 2 * kTreePartialFloats
 // storage rows (positions; slots of a ring) base + 64 (h - 1) .., of which
 // [lo, hi) hold tokens that some node attends.
 constexpr int kMaxTreeUnits = FLINT_MAX_BATCH * (kMaxTree / 32);
-struct TreeUnit {
+struct alignas(32) TreeUnit {
   int16_t b;
   int8_t rb, mt;
   int8_t dup;                // copies of the rows in the row tile
+  int8_t nodes;              // the request's nodes
   int32_t base, lo, hi;
   int32_t halves, tiles;
+  int32_t len;               // the request's committed tokens
   int16_t q0, q1;            // the groups that hold a share of it
 };
 struct TreeCut {
