@@ -476,10 +476,12 @@ size_t flint_tree_workspace_bytes(int32_t num_ctas);
  * N in [1, FLINT_MAX_TREE], B in [1, FLINT_MAX_BATCH].  Scores and sums are
  * fp32; the probabilities and v enter their product in fp16 (v saturating at
  * +-65504, exact for bf16 values in the fp16 normal range, as in the
- * prefill), and with an E4M3 cache q in fp16 too.  Cache slots outside the
- * attended range may hold anything.  Results are the same run to run for
- * given lengths, N and num_ctas.  Paged block ids and time-outs as for
- * flint_attn_decode. */
+ * prefill).  With an E4M3 cache each row of q is held to 2^-17 of its largest
+ * magnitude, in two E4M3 terms.  Cache slots outside the attended range may
+ * hold anything; a k or v that is NaN makes outputs NaN for the nodes that
+ * attend it and leaves the others as they are.  Results are the same run to
+ * run for given lengths, N, n_draft and num_ctas.  Paged block ids and time-outs as for
+ * flint_attn_decode (nothing in the workspace needs zeroing after one). */
 flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const uint16_t* v_draft,
                              const int32_t* parent, int32_t N, const flint_kv_cache* cache,
                              const int32_t* seq_lens, const int32_t* n_draft, int32_t B,
@@ -533,6 +535,19 @@ flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_laye
                                   const int32_t* path, const int32_t* n_accepted, int32_t N,
                                   const int32_t* seq_lens, int32_t B, int32_t* dev_err,
                                   void* stream);
+
+/* The plan of a flint_attn_tree call (pure host code, exposed for tests).  Units
+ * are blocks of up to 32 nodes of a request, in order, over tiles of 128 keys;
+ * groups of four CTAs take contiguous shares of all tiles.
+ *   units [max_units][4]   request, node block, tiles, row tiles (1 or 2)
+ *   cuts  [max_groups + 1][2]  unit and tile where each group begins; the last
+ *                          row is (units, 0)
+ * Returns the number of groups (0: nothing to do; no group is empty), with
+ * *n_units the number of units, or -1 for invalid arguments or arrays that are
+ * too small. */
+int32_t flint_plan_tree(const int32_t* seq_lens, const int32_t* n_draft, int32_t B, int32_t window,
+                        int32_t layout, int32_t fp8, int32_t num_ctas, int32_t* units, int32_t max_units,
+                        int32_t* n_units, int32_t* cuts, int32_t max_groups);
 
 /* The split planner behind both attention calls (pure host code, exposed for
  * tests).  Work is n_segs segments (one per problem, all four KV heads

@@ -230,6 +230,39 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   return launched(launch_tree(p, static_cast<cudaStream_t>(stream)), who);
 }
 
+int32_t flint_plan_tree(const int32_t* seq_lens, const int32_t* n_draft, int32_t B, int32_t window, int32_t layout, int32_t fp8,
+                        int32_t num_ctas, int32_t* units, int32_t max_units, int32_t* n_units, int32_t* cuts, int32_t max_groups) {
+  if (!seq_lens || !n_draft || !units || !n_units || !cuts || B < 1 || B > FLINT_MAX_BATCH || num_ctas < 1 || num_ctas > kMaxCtas ||
+      (window != 0 && window != kWindow) || layout < FLINT_KV_CONTIGUOUS || layout > FLINT_KV_PAGED)
+    return -1;
+  static thread_local TreeParams p;
+  memset(&p, 0, sizeof p);
+  for (int b = 0; b < B; ++b) {
+    if (seq_lens[b] < 0 || seq_lens[b] > FLINT_MAX_CONTEXT || n_draft[b] < 0 || n_draft[b] > FLINT_MAX_TREE) return -1;
+    p.len[b] = seq_lens[b];
+    p.n_draft[b] = static_cast<int8_t>(n_draft[b]);
+  }
+  p.B = B;
+  p.N = FLINT_MAX_TREE;
+  p.window = window;
+  p.layout = layout;
+  p.fp8 = fp8 != 0;
+  plan_tree(p, std::max(1, num_ctas / kKvHeads));
+  if (p.n_units > max_units || p.n_groups > max_groups) return -1;
+  *n_units = p.n_units;
+  for (int u = 0; u < p.n_units; ++u) {
+    units[4 * u] = p.unit[u].b;
+    units[4 * u + 1] = p.unit[u].rb;
+    units[4 * u + 2] = p.unit[u].tiles;
+    units[4 * u + 3] = p.unit[u].mt;
+  }
+  for (int q = 0; q <= p.n_groups; ++q) {
+    cuts[2 * q] = p.cut[q].unit;
+    cuts[2 * q + 1] = p.cut[q].tile;
+  }
+  return p.n_groups;
+}
+
 flint_status flint_verify_tree(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
                                const int32_t* tokens, const int32_t* parent, const int32_t* n_draft, int32_t B, int32_t N,
                                int32_t V, const float* u_accept, const float* u_sample, int32_t* path,

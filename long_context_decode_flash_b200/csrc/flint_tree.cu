@@ -52,6 +52,11 @@
 
 namespace flint {
 
+#ifdef FLINT_TEST_HOOKS
+// {block, K tile}: that CTA's producer leaves that K tile unarmed; {-1, -1} = off.
+__device__ int g_stall_tree[2] = {-1, -1};
+#endif
+
 namespace {
 
 constexpr int kTrRows = 128;               // rows of a row tile: 16 nodes x 8 heads
@@ -335,6 +340,9 @@ __device__ __forceinline__ bool run_tma(const TreeParams& p, int q, int g, uint3
         now = ahead;
         ahead = pages((j >> 4) + 1);
       }
+#ifdef FLINT_TEST_HOOKS
+      if (!kV && static_cast<int>(blockIdx.x) == g_stall_tree[0] && it.T + j == g_stall_tree[1]) continue;
+#endif
       const int h = h0 + 2 * j;
       const bool box0 = h >= 1, box1 = h + 1 < h1;  // (box 0 exists behind half 0: h < h1)
       const int row0 = paged ? 0 : un.base + (h - 1) * kHalf, row1 = paged ? 0 : row0 + kHalf;
@@ -1279,6 +1287,15 @@ void plan_tree(TreeParams& p, int num_groups) {
     p.split |= cut;
   }
 }
+
+#ifdef FLINT_TEST_HOOKS
+// Test builds only: CTA `block` leaves its K tile `tile` unarmed; block = -1
+// turns the hook off.
+extern "C" int flint_test_stall_tree(int block, int tile) {
+  const int v[2] = {block, tile};
+  return static_cast<int>(cudaMemcpyToSymbol(g_stall_tree, v, sizeof v));
+}
+#endif
 
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   if (p.n_units == 0) return cudaSuccess;

@@ -37,7 +37,7 @@ EXPORTED = (
     "flint_attn_stack_noalloc", "flint_attn_layers_serial", "flint_plan_items", "flint_plan_split",
     "flint_prefill_qk_norm_rope", "flint_prefill_attn", "flint_attn_decode_partial",
     "flint_merge_partials", "flint_qk_norm_rope_at", "flint_tree_workspace_bytes", "flint_attn_tree",
-    "flint_verify_tree", "flint_kv_append_path",
+    "flint_verify_tree", "flint_kv_append_path", "flint_plan_tree",
 )
 MAX_TREE = 64
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
@@ -123,6 +123,8 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.flint_attn_tree.argtypes = [P, P, P, P, I32, P, P, P, I32, P, I32, P, P, ctypes.c_size_t, I32, P, P]
     lib.flint_verify_tree.argtypes = [P, I64, P, I64, P, P, P, I32, I32, I32, P, P, P, P, P, P, P]
     lib.flint_kv_append_path.argtypes = [P, I32, P, P, I32, P, I32, P, P]
+    lib.flint_plan_tree.argtypes = [P, P, I32, I32, I32, I32, I32, P, I32, P, P, I32]
+    lib.flint_plan_tree.restype = I32
     lib.flint_plan_items.argtypes = [P, I32, I32, I32, P, P, P, P, I32]
     lib.flint_plan_items.restype = I32
     lib.flint_plan_split.argtypes = [P, I32, I32, I32, I32, P, P, P, P, P]
@@ -134,7 +136,8 @@ def open_library(path: str) -> ctypes.CDLL:
                  "flint_kv_append_path"):
         getattr(lib, name).restype = ctypes.c_int
     # test builds only (libflint_hooks.so): leave one pipeline stage unarmed
-    for name in ("flint_test_stall_decode", "flint_test_stall_prefill", "flint_test_stall_prefill_prep"):
+    for name in ("flint_test_stall_decode", "flint_test_stall_prefill", "flint_test_stall_prefill_prep",
+                 "flint_test_stall_tree"):
         if hasattr(lib, name):
             getattr(lib, name).argtypes = [ctypes.c_int, ctypes.c_int]
             getattr(lib, name).restype = ctypes.c_int
@@ -538,6 +541,20 @@ def flint_kv_append_path(layers, path, n_accepted, seq_lens: Sequence[int], dev_
     _check(load_library().flint_kv_append_path(
         arr, len(arr), _dense(path, torch.int32, (B, N), "path", dev), _dense(n_accepted, torch.int32, (B,), "n_accepted", dev), N,
         lens.buffer_info()[0], B, _error_word(dev_err, dev), _stream_of(stream, dev)))
+
+
+def flint_plan_tree(seq_lens: Sequence[int], n_draft: Sequence[int], window: int = 0, layout: int = CONTIGUOUS, fp8: bool = False,
+                    num_ctas: int = 148):
+    """The plan of a flint_attn_tree call: (units [(request, node block, tiles, row
+    tiles)], cuts [(unit, tile)] of the groups and the end)."""
+    B, max_units, max_groups = len(seq_lens), 128, 74
+    lens, counts = _host_i32(seq_lens, B, "seq_lens"), _host_i32(n_draft, B, "n_draft")
+    units, cuts, n = (ctypes.c_int32 * (4 * max_units))(), (ctypes.c_int32 * (2 * max_groups + 2))(), ctypes.c_int32()
+    groups = load_library().flint_plan_tree(lens.buffer_info()[0], counts.buffer_info()[0], B, int(window), int(layout), int(fp8),
+                                            int(num_ctas), units, max_units, ctypes.byref(n), cuts, max_groups)
+    _need(groups >= 0, "flint_plan_tree: invalid arguments")
+    return ([tuple(units[4 * u:4 * u + 4]) for u in range(n.value)],
+            [tuple(cuts[2 * q:2 * q + 2]) for q in range(groups + 1)])
 
 
 def flint_plan_items(seg_tiles: Sequence[int], num_ctas: int, item_cost: int = 2,
