@@ -114,13 +114,15 @@ struct TreeParams {
   int32_t len[FLINT_MAX_BATCH];
   int8_t n_draft[FLINT_MAX_BATCH];
   int32_t N, B, window;
-  int32_t n_units, n_groups, split;  // split: some unit leaves partials
+  int32_t n_units, n_groups;
+  int32_t n_cut, cut_nodes;          // units that leave partials, and the most nodes of one
   TreeUnit unit[kMaxTreeUnits];
   TreeCut cut[kMaxTreeGroups + 1];   // group q: from cut[q] to cut[q + 1]
+  int16_t cut_unit[kMaxTreeGroups];  // the units that leave partials
   int32_t* dev_err;
 };
 static_assert(sizeof(TreeParams) <= 32000, "kernel parameters exceed 32 KiB");
-// Fills unit, cut, n_units, n_groups and split from len, n_draft, B, window,
+// Fills unit, cut, cut_unit and their counts from len, n_draft, B, window,
 // layout and fp8, for at most num_groups groups of CTAs.
 void plan_tree(TreeParams& p, int num_groups);
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);

@@ -1128,11 +1128,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   __shared__ float2 wt[kJoinMax][kGroup];  // m (then 2^(m - M)), l
   __shared__ float ltot[kGroup], mtop[kGroup];
   __shared__ float4 sum[kJoinShares - 1][kGroup * 8];
-  const int g = blockIdx.x % kKvHeads, u = blockIdx.z;
+  const int g = blockIdx.x % kKvHeads, u = p.cut_unit[blockIdx.z];
   const TreeUnit& un = p.unit[u];
   const int nd = blockIdx.x / kKvHeads, b = un.b, node = un.rb * 2 * kTrNodes + nd;
   const int q0 = un.q0, shift = un.dup >> 1;  // dup 1, 2: 0, 1
-  if (q0 == un.q1 || node >= un.nodes) return;
+  if (node >= un.nodes || nd >= 2 * kTrNodes) return;
   const int parts = (un.q1 - q0 + 1) << shift;
   const int r0 = (nd & (kTrNodes - 1)) * kGroup;
   // only the unit's first group may hold it as a later item than its first
@@ -1284,7 +1284,7 @@ void plan_tree(TreeParams& p, int num_groups) {
   }
   p.n_groups = groups - 1;
   // the groups with a share of each unit (no group is empty: they are a range)
-  p.split = 0;
+  p.n_cut = p.cut_nodes = 0;
   int q = 0;
   for (int x = 0; x < n_units; ++x) {
     while (p.cut[q + 1].unit < x || (p.cut[q + 1].unit == x && p.cut[q + 1].tile == 0)) ++q;
@@ -1294,7 +1294,10 @@ void plan_tree(TreeParams& p, int num_groups) {
     const bool cut = p.unit[x].q1 > p.unit[x].q0;
     const int nodes = p.n_draft[p.unit[x].b] - p.unit[x].rb * 2 * kTrNodes;
     p.unit[x].dup = cut && nodes <= kTrNodes / 2 ? 2 : 1;
-    p.split |= cut;
+    if (cut) {
+      p.cut_unit[p.n_cut++] = static_cast<int16_t>(x);
+      p.cut_nodes = std::max(p.cut_nodes, std::min(nodes, 2 * kTrNodes));
+    }
   }
 }
 
@@ -1310,15 +1313,11 @@ extern "C" int flint_test_stall_tree(int block, int tile) {
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   if (p.n_units == 0) return cudaSuccess;
   bool two = false;
-  int nodes = 0;
-  for (int b = 0; b < p.B; ++b) {
-    two |= p.n_draft[b] > kTrNodes;
-    nodes = std::max(nodes, static_cast<int>(p.n_draft[b]));
-  }
+  for (int b = 0; b < p.B; ++b) two |= p.n_draft[b] > kTrNodes;
   const cudaError_t e = two ? (p.fp8 ? launch_one<2, true>(p, stream) : launch_one<2, false>(p, stream))
                             : (p.fp8 ? launch_one<1, true>(p, stream) : launch_one<1, false>(p, stream));
-  if (e != cudaSuccess || !p.split) return e;
-  return launch_overlapped(dim3(std::min(nodes, 2 * kTrNodes) * kKvHeads, 4, p.n_units), kJoinThreads, 0, stream, tree_join_kernel, p);
+  if (e != cudaSuccess || p.n_cut == 0) return e;
+  return launch_overlapped(dim3(p.cut_nodes * kKvHeads, 4, p.n_cut), kJoinThreads, 0, stream, tree_join_kernel, p);
 }
 
 }  // namespace flint
