@@ -79,7 +79,9 @@ constexpr size_t kTreeGroupBytes = size_t(kKvHeads) * 2 * 2 * kTreePartialFloats
 // A unit: up to 32 nodes of a request (mt row tiles of 16) against its keys, in
 // tiles of two 64-key halves: half 0 the drafted tokens, half h >= 1 the cache's
 // storage rows (positions; slots of a ring) base + 64 (h - 1) .., of which
-// [lo, hi) hold tokens that some node attends.
+// [lo, hi) hold tokens that some node attends.  The part_n rows from part on (of a
+// ring: modulo its 513 slots) are those that some node may not attend: a window's
+// oldest, and the slot before them.
 constexpr int kMaxTreeUnits = FLINT_MAX_BATCH * (kMaxTree / 32);
 struct alignas(32) TreeUnit {
   int16_t b;
@@ -89,6 +91,7 @@ struct alignas(32) TreeUnit {
   int32_t base, lo, hi;
   int32_t halves, tiles;
   int32_t len;               // the request's committed tokens
+  int32_t part, part_n;
   int16_t q0, q1;            // the groups that hold a share of it
 };
 struct TreeCut {

@@ -291,6 +291,18 @@ __device__ __forceinline__ bool next_item(const TreeParams& p, int q, Item& it) 
   return clip(p, q, it);
 }
 
+// Some node may not attend storage row s (TreeUnit::part).
+__device__ __forceinline__ bool row_in_part(const TreeParams& p, const TreeUnit& un, int s) {
+  int t = s - un.part;
+  if (p.layout == FLINT_KV_RING && t < 0) t += kWindow;
+  return t >= 0 && t < un.part_n;
+}
+// Every node attends every key of the unit's tile t.
+__device__ __forceinline__ bool tile_whole(const TreeParams& p, const TreeUnit& un, int t) {
+  const int s0 = un.base + (2 * t - 1) * kHalf, s1 = s0 + kTrKeys, end = un.part + un.part_n;
+  return t > 0 && s0 >= un.lo && s1 <= un.hi && (un.part_n == 0 || ((un.part >= s1 || end <= s0) && (p.layout != FLINT_KV_RING || end - kWindow <= s0)));
+}
+
 // The order of an item's 2 n operand tiles is that of their first use.  Two row
 // tiles: K0 V0 K1 V1 ..; one (S runs two key tiles ahead): K0 K1 V0 K2 V1 .. V.
 __device__ __forceinline__ int seq_of(bool v, int j, int n, int mt) {
@@ -575,7 +587,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
       } else {
         const int s = un.base + (h - 1) * kHalf + j;
         token = h < un.halves && s >= un.lo && s < un.hi;
-        scan = token && p.window > 0 && (p.layout == FLINT_KV_RING || s < un.lo + kMaxTree);
+        scan = token && row_in_part(p, un, s);
       }
       uint8_t* tile;
       uint32_t half_rows = 0;  // record of the drafts' rows' second halves
@@ -750,11 +762,11 @@ __device__ __forceinline__ void run_mma(const TreeParams& p, int q, uint32_t bas
     if (globaltimer_ns() - t0 > kWaitLimitNs) break;
 }
 
-// Bits j of 32 with lo <= k0 + j < hi.
-__device__ __forceinline__ uint32_t range_bits(int k0, int lo, int hi) {
-  const int a = min(max(lo - k0, 0), 32), e = min(max(hi - k0, 0), 32);
-  const uint32_t upto = e >= 32 ? 0xffffffffu : (1u << e) - 1u, from = a >= 32 ? 0xffffffffu : (1u << a) - 1u;
-  return upto & ~from;
+// Bits j of 64 with lo <= k0 + j < hi.
+__device__ __forceinline__ unsigned long long range_bits(int k0, int lo, int hi) {
+  const int a = min(max(lo - k0, 0), 64), e = min(max(hi - k0, 0), 64);
+  if (a >= e) return 0ull;
+  return ~0ull >> (64 - e) & ~0ull << a;
 }
 
 // What a softmax thread knows of its row.
@@ -808,25 +820,33 @@ __device__ __forceinline__ unsigned long long tree_line(const TreeParams& p, int
   return from(line[0], line[1], node);
 }
 
-// The mask word of keys 32 k .. 32 k + 31 of tile t for a row.
-__device__ __forceinline__ uint32_t mask_word(const TreeParams& p, const TreeUnit& un, const Row& row, int t, int k) {
-  const int h = 2 * t + (k >> 1);
-  if (h == 0) return static_cast<uint32_t>(row.line >> (32 * (k & 1)));
-  if (h >= un.halves) return 0u;
-  const int s0 = un.base + (h - 1) * kHalf + 32 * (k & 1);
+// The mask of half h (of the unit) for a row.
+__device__ __forceinline__ unsigned long long half_mask(const TreeParams& p, const TreeUnit& un, const Row& row, int h) {
+  if (h == 0) return row.line;
+  if (h >= un.halves) return 0ull;
+  const int s0 = un.base + (h - 1) * kHalf;
   if (p.layout == FLINT_KV_RING) return range_bits(s0, row.r0, min(row.r1, kWindow)) | range_bits(s0, 0, row.r1 - kWindow);
   return range_bits(s0, row.lo, row.hi);
 }
 
 // One step of a row: S to P (P's pairs lie over their own 32-key chunk of S),
 // and O brought to the new maximum where it moved.  The row's scores stay in
-// registers (one TMEM wait).  Chunks outside `mine` (a bit a chunk) belong to
+// registers (one TMEM wait).  masked: keys outside `mask` are not attended; lost:
+// one that is has NaN in v, and the row becomes NaN.  Chunks outside `mine` (a bit a chunk) belong to
 // the row's other copy and get probability 0.
-__device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float scale, uint32_t mine, bool first, float& m, float& l) {
+__device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float scale, uint32_t mine, bool first, bool masked,
+                                             const uint4& mask, bool lost, float& m, float& l) {
   uint32_t v[4][32];
 #pragma unroll
   for (int k = 0; k < 4; ++k) tmem_ld32(sp + 32 * k, v[k]);
   tmem_wait_ld();
+  if (masked) {
+    const uint32_t words[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[k][i] = words[k] & 1u << i ? v[k][i] : 0xff800000u;
+  }
   float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int k = 0; k < 4; k += 2)
@@ -835,7 +855,7 @@ __device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float sca
       for (int i = 0; i < 64; i += 2)
         mq[(i >> 1) & 3] = max3_nan(mq[(i >> 1) & 3], __uint_as_float(v[k + (i >> 5)][i & 31]), __uint_as_float(v[k + (i >> 5)][(i & 31) + 1]));
     }
-  const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]) * scale - kBias;
+  const float mx = lost ? NAN : max3_nan(max3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]) * scale - kBias;
   float factor = 1.f;
   const bool need = !(mx <= m + kTau) && mx != -INFINITY;  // (NaN needs)
   if (need) {
@@ -901,9 +921,6 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   row.hi = L;
   row.r0 = row.lo % kWindow;
   row.r1 = row.r0 + max(0, L - row.lo);
-  // from here on every node attends all of [.., L)
-  const int lo_all = p.window > 0 ? un.lo + kMaxTree : 0;
-
   const uint32_t mine = dup == 1 ? 15u : 3u << 2 * copy;
   if (FP8) {
     if (!warp_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, B)) return false;
@@ -920,24 +937,17 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
     if (work) {
       const int t = it.t0 + ti, T = it.T + ti;
       const uint32_t sp = lane_base + kColS + 128 * w, op = lane_base + kColO + 128 * w;
-      const int s_lo = un.base + (2 * t - 1) * kHalf;
-      if (p.layout == FLINT_KV_RING || t == 0 || s_lo < lo_all || s_lo + kTrKeys > L) {
-        // some key is not attended by some row: such scores become -inf, and NaN
-        // those of attended keys whose v is not finite (recorded when V is an operand)
+      const bool masked = !tile_whole(p, un, t);
+      uint4 mask = make_uint4(0, 0, 0, 0);
+      bool lost = false;  // an attended key's v is NaN (recorded when V is an operand)
+      if (masked) {
+        const unsigned long long lo = half_mask(p, un, row, 2 * t), hi = half_mask(p, un, row, 2 * t + 1);
+        mask = make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
         if (!warp_wait(smem_u32(&B->v_ready[T & 3]), static_cast<uint32_t>(T >> 2) & 1u, B)) return false;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32];
-          tmem_ld32(sp + 32 * k, v);
-          const uint32_t mask = mask_word(p, un, row, t, k), lost = (losts[(T % kInfo) * 8 + k] | (k < 2 ? losts[(T % kInfo) * 8 + 4 + k] : 0u)) & mask;
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = lost >> i & 1u ? 0x7fc00000u : mask >> i & 1u ? v[i] : 0xff800000u;
-          tmem_st32(sp + 32 * k, v);
-        }
-        tmem_wait_st();
+        const uint32_t* rec = losts + (T % kInfo) * 8;
+        lost = (((rec[0] | rec[4]) & mask.x) | ((rec[1] | rec[5]) & mask.y) | (rec[2] & mask.z) | (rec[3] & mask.w)) != 0u;
       }
-      softmax_step(sp, op, scale, mine, s == 0, m, l);
+      softmax_step(sp, op, scale, mine, s == 0, masked, mask, lost, m, l);
     }
     tc_fence_before();
     __syncwarp();
@@ -1263,6 +1273,10 @@ void plan_tree(TreeParams& p, int num_groups) {
       u.base = p.layout == FLINT_KV_RING ? 0 : p.layout == FLINT_KV_PAGED ? lo / kBlock * kBlock : lo;
       u.lo = p.layout == FLINT_KV_RING ? 0 : lo;
       u.hi = p.layout == FLINT_KV_RING ? std::min(L, kWindow) : L;
+      const int left = std::max(0, L - kWindow), deep = std::max(0, L - (p.window - 1) + p.n_draft[b] - 1);  // positions
+      const bool ring = p.layout == FLINT_KV_RING;
+      u.part = ring ? left % kWindow : lo;
+      u.part_n = p.window == 0 ? 0 : std::min(L, deep) - (ring ? left : lo);
       u.halves = 1 + (u.hi - u.base + kHalf - 1) / kHalf;
       u.tiles = (u.halves + 1) / 2;
       cost[n_units] = p.fp8 ? u.mt : 1;
