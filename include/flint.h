@@ -537,8 +537,8 @@ flint_status flint_kv_append_path(const flint_path_layer* layers, int32_t n_laye
                                   void* stream);
 
 /* The plan of a flint_attn_tree call (pure host code, exposed for tests).  Units
- * are blocks of up to 32 nodes of a request, in order, over tiles of 128 keys;
- * groups of four CTAs take contiguous shares of all tiles.
+ * are blocks of up to 32 nodes of a request over tiles of 128 keys; groups of
+ * four CTAs take contiguous shares of all tiles, or whole units dealt by size.
  *   units [max_units][4]   request, node block, tiles, row tiles (1 or 2)
  *   cuts  [max_groups + 1][2]  unit and tile where each group begins; the last
  *                          row is (units, 0)

@@ -1253,6 +1253,11 @@ cudaError_t launch_one(const TreeParams& p, cudaStream_t stream) {
 // the drafts are converted.  64 nodes, batch of 4: 137 us with 2, 132 with 8, 129
 // with 12; bf16 measures the same from 2 to 12.)
 constexpr int kUnitCost = 4, kUnitCostE4m3 = 12;
+// What the second launch and the partials cost, in the same measure, for one unit;
+// half as much more for each unit beside it, up to 17.  (Windows of 513 of 32
+// requests with 8 nodes: 16.0 us whole, 28.5 cut; of one request: 13.2 whole, 9.9
+// cut; 64 requests of 100 to 4,000 tokens: 56 whole, 69 cut.)
+constexpr int kJoinCost = 3;
 
 void plan_tree(TreeParams& p, int num_groups) {
   // Units, and what a tile of each costs: with E4M3 a tile is bound by the
@@ -1287,14 +1292,42 @@ void plan_tree(TreeParams& p, int num_groups) {
   }
   begin[n_units] = total;
   p.n_units = n_units;
-  // Equal shares, cut at whole tiles; a share without a tile falls away.
-  int u = 0, groups = 0;
-  for (int k = 0; k <= num_groups; ++k) {
-    const int64_t at = total * k / num_groups;
-    while (u < n_units && begin[u + 1] <= at) ++u;
-    const TreeCut c{static_cast<int16_t>(u), static_cast<int16_t>(u < n_units ? std::max<int64_t>(0, at - begin[u] - unit_cost) / cost[u] : 0)};
-    if (groups > 0 && p.cut[groups - 1].unit == c.unit && p.cut[groups - 1].tile == c.tile) continue;
-    p.cut[groups++] = c;
+  int groups = 0;
+  // Whole units, the longest first, each to the group with the least ...
+  int order[kMaxTreeUnits], of[kMaxTreeUnits];
+  for (int u = 0; u < n_units; ++u) order[u] = u;
+  auto cost_of = [&](int u) { return begin[u + 1] - begin[u]; };
+  std::stable_sort(order, order + n_units, [&](int a, int b) { return cost_of(a) > cost_of(b); });
+  int64_t load[kMaxTreeGroups] = {}, fullest = 0;
+  const int usable = std::min(num_groups, n_units);
+  for (int i = 0; i < n_units; ++i) {
+    const int g = static_cast<int>(std::min_element(load, load + usable) - load);
+    of[order[i]] = g;
+    load[g] += cost_of(order[i]);
+    fullest = std::max(fullest, load[g]);
+  }
+  // ... where that takes no longer than even shares and their join
+  const int64_t join = kJoinCost + std::min(17, n_units / 2);
+  if (n_units > 0 && fullest <= std::max<int64_t>(total / num_groups, unit_cost + 1) + join) {
+    TreeUnit unit[kMaxTreeUnits];
+    std::copy(p.unit, p.unit + n_units, unit);
+    int n = 0;
+    for (int g = 0; g < usable; ++g) {
+      p.cut[groups++] = TreeCut{static_cast<int16_t>(n), 0};
+      for (int u = 0; u < n_units; ++u)
+        if (of[u] == g) p.unit[n++] = unit[u];
+    }
+    p.cut[groups++] = TreeCut{static_cast<int16_t>(n), 0};
+  } else {
+    // Equal shares, cut at whole tiles; a share without a tile falls away.
+    int u = 0;
+    for (int k = 0; k <= num_groups; ++k) {
+      const int64_t at = total * k / num_groups;
+      while (u < n_units && begin[u + 1] <= at) ++u;
+      const TreeCut c{static_cast<int16_t>(u), static_cast<int16_t>(u < n_units ? std::max<int64_t>(0, at - begin[u] - unit_cost) / cost[u] : 0)};
+      if (groups > 0 && p.cut[groups - 1].unit == c.unit && p.cut[groups - 1].tile == c.tile) continue;
+      p.cut[groups++] = c;
+    }
   }
   p.n_groups = groups - 1;
   // the groups with a share of each unit (no group is empty: they are a range)

@@ -31,7 +31,7 @@ def test_every_tile_once(seed):
     ctas = rng.choice([1, 4, 7, 60, 148, 296])
     units, cuts = flint.flint_plan_tree(lens, n, window, layout, rng.random() < 0.5, ctas)
     want = [(b, r, tiles_of(lens[b], window, layout), 2 if n[b] - 32 * r > 16 else 1) for b in range(B) for r in range(-(-n[b] // 32))]
-    assert units == want
+    assert sorted(units) == want  # (units that stay whole are dealt by size)
     if not units:
         assert cuts == [(0, 0)] and len(cuts) == 1
         return
