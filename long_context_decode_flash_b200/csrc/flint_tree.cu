@@ -11,9 +11,10 @@
 // keys come in tiles of 128, two 64-key halves each: half 0 is the drafted
 // tokens themselves, the halves behind it 64-token boxes of the cache (whole
 // pages of a paged cache, slots of a ring).  Groups of four CTAs, one per KV
-// head, take contiguous shares of all (unit, tile) pairs, so that the four
-// read the same token rows at the same time; a unit cut between groups leaves
-// one partial per share (O, m, l), and a second launch folds them in order.
+// head, so that the four read the same token rows at the same time, take either
+// whole units, dealt by size, or contiguous shares of all (unit, tile) pairs,
+// whichever the plan finds shorter; a unit cut between groups leaves one partial
+// per share (O, m, l), and a second launch folds them in order.
 //
 // A CTA is 15 working warps over two streams of steps, a step being one row tile
 // against one key tile.  Two row tiles: stream w is row tile w.  One row tile:
@@ -51,7 +52,7 @@
 // takes the clock from 1,965 to ~1,500 MHz); else a row tile's chain softmax ->
 // PV -> S -> softmax, 4,400 cycles over two streams, ~2,200 a step where the MMAs
 // alone take 1,024 and the exponentials (16 a clock) 1,024 (30 nodes, E4M3, 100,000
-// tokens: 75 us; 64 nodes, batch of 4: 129 us).  A launch's first and last 4 to 5 us
+// tokens: 73 us; 64 nodes, batch of 4: 124 us).  A launch's first and last 4 to 5 us
 // are set-up, the first tile, the end of the item and the join.
 #include <math.h>
 
@@ -97,10 +98,12 @@ constexpr int kInfo = 4;                   // tiles whose record of non-finite v
 // codes and of V's fp16 tiles.
 template <int MT, bool FP8>
 struct Lay {
-  static constexpr int kTiles = FP8 ? (MT == 1 ? 4 : 3) : (MT == 1 ? 6 : 5);  // bf16 K and V, or K codes
+  static constexpr int kTiles = FP8 ? 3 : MT == 1 ? 6 : 5;  // bf16 K and V, or K codes
   static constexpr uint32_t kTileBytes = FP8 ? kCodes : kStage;
-  static constexpr int kRaws = MT == 1 ? 4 : 3;                               // E4M3: V's codes, the drafts
-  static constexpr int kVs = 2;                                               // E4M3: V in fp16
+  static constexpr int kRaws = 3;                             // E4M3: V's codes, the drafts
+  // E4M3: V in fp16.  (One row tile: two streams' tiles are in use at once, and a
+  // third lets the converters work ahead: 16 requests x 12 nodes 182 -> 180 us.)
+  static constexpr int kVs = MT == 1 ? 3 : 2;
   static constexpr uint32_t kTile = MT * kQTile;
   static constexpr uint32_t kRaw = kTile + kTiles * kTileBytes;
   static constexpr uint32_t kV = kRaw + (FP8 ? kRaws * kCodes : 0);
@@ -116,7 +119,7 @@ static_assert(Lay<1, false>::kBytes <= 232448 && Lay<2, false>::kBytes <= 232448
 struct Bars {
   uint64_t full[6], empty[6];            // a tile (E4M3: K tile) landed; was consumed
   uint64_t raw_full[4], raw_free[4];     // E4M3: V's codes, or drafts, landed; were read
-  uint64_t v_empty[2];                   // E4M3: an fp16 V tile was consumed
+  uint64_t v_empty[3];                   // E4M3: an fp16 V tile was consumed
   uint64_t v_ready[4];                   // V of tile T (mod 4) is an operand
   uint64_t kd_ready;                     // E4M3, per item that begins its unit: the drafts' K codes written
   uint64_t s_full[2];                    // S_w complete (and every MMA issued before it)
@@ -832,25 +835,30 @@ __device__ __forceinline__ unsigned long long half_mask(const TreeParams& p, con
 // One step of a row: S to P (P's pairs lie over their own 32-key chunk of S),
 // and O brought to the new maximum where it moved.  The row's scores stay in
 // registers (one TMEM wait).  masked: keys outside `mask` are not attended; lost:
-// one that is has NaN in v, and the row becomes NaN.  Chunks outside `mine` (a bit a chunk) belong to
-// the row's other copy and get probability 0.
-__device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float scale, uint32_t mine, bool first, bool masked,
+// one that is has NaN in v, and the row becomes NaN.  The row's chunks are the nk
+// from kb on (all four, or its copy's two; the same for a warp); the others get
+// probability 0.  (A bit mask of chunks tested at each use instead, and all four
+// always loaded: 16 requests x 12 nodes 180 us for 173, 4 x 64 nodes 130 for 124.)
+__device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float scale, int kb, int nk, bool first, bool masked,
                                              const uint4& mask, bool lost, float& m, float& l) {
   uint32_t v[4][32];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) tmem_ld32(sp + 32 * k, v[k]);
+  for (int k = 0; k < 4; ++k)
+    if (k < nk) tmem_ld32(sp + 32 * (kb + k), v[k]);
   tmem_wait_ld();
   if (masked) {
-    const uint32_t words[4] = {mask.x, mask.y, mask.z, mask.w};
+    const uint32_t words[4] = {kb ? mask.z : mask.x, kb ? mask.w : mask.y, mask.z, mask.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
+      if (k < nk) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[k][i] = words[k] & 1u << i ? v[k][i] : 0xff800000u;
+        for (int i = 0; i < 32; ++i) v[k][i] = words[k] & 1u << i ? v[k][i] : 0xff800000u;
+      }
   }
   float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int k = 0; k < 4; k += 2)
-    if (mine >> k & 1u) {
+    if (k < nk) {
 #pragma unroll
       for (int i = 0; i < 64; i += 2)
         mq[(i >> 1) & 3] = max3_nan(mq[(i >> 1) & 3], __uint_as_float(v[k + (i >> 5)][i & 31]), __uint_as_float(v[k + (i >> 5)][(i & 31) + 1]));
@@ -867,8 +875,8 @@ __device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float sca
   float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t pk[16];
-    if (mine >> k & 1u) {
+    if (k < nk) {
+      uint32_t pk[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const float2 x = fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), scale2, nmu);
@@ -877,11 +885,13 @@ __device__ __forceinline__ void softmax_step(uint32_t sp, uint32_t op, float sca
         const __half2 hp = __floats2half2_rn(e.x, e.y);
         pk[c] = *reinterpret_cast<const uint32_t*>(&hp);
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) pk[c] = 0u;
+      tmem_st16(sp + 32 * (kb + k), pk);
     }
-    tmem_st16(sp + 32 * k, pk);
+  }
+  if (nk == 2) {
+    const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    tmem_st16(sp + 32 * (kb ^ 2), zero);
+    tmem_st16(sp + 32 * (kb ^ 2) + 32, zero);
   }
   const float2 lsum = add2(ls[0], ls[1]);
   l += lsum.x + lsum.y;
@@ -906,7 +916,7 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   using Y = Lay<MT, FP8>;
   const TreeUnit& un = p.unit[it.u];
   const int w = warp >> 2, b = un.b, n = un.nodes, L = un.len, two = it.mt == 2, dup = un.dup;
-  const int r = (warp & 3) * 32 + lane, copy_rows = kTrRows / dup, copy = r / copy_rows;
+  const int r = (warp & 3) * 32 + lane, copy_rows = kTrRows / dup, copy = (warp & 3) * 32 / copy_rows;
   const int tile0 = un.rb * 2 * kTrNodes + (two ? w * kTrNodes : 0);  // first node of this row tile
   const int node = tile0 + ((r & (copy_rows - 1)) >> 3), h = g * kGroup + (r & 7);
   const bool work = __any_sync(0xffffffffu, node < n);  // some row of this warp is a node's
@@ -921,7 +931,6 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   row.hi = L;
   row.r0 = row.lo % kWindow;
   row.r1 = row.r0 + max(0, L - row.lo);
-  const uint32_t mine = dup == 1 ? 15u : 3u << 2 * copy;
   if (FP8) {
     if (!warp_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, B)) return false;
     const int e = reinterpret_cast<const int8_t*>(smem + Y::kQExp)[(two ? w * kTrRows : 0) + r];
@@ -947,7 +956,7 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
         const uint32_t* rec = losts + (T % kInfo) * 8;
         lost = (((rec[0] | rec[4]) & mask.x) | ((rec[1] | rec[5]) & mask.y) | (rec[2] & mask.z) | (rec[3] & mask.w)) != 0u;
       }
-      softmax_step(sp, op, scale, mine, s == 0, masked, mask, lost, m, l);
+      softmax_step(sp, op, scale, 2 * copy, dup == 1 ? 4 : 2, s == 0, masked, mask, lost, m, l);
     }
     tc_fence_before();
     __syncwarp();
@@ -1046,8 +1055,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
       mbar_init(smem_u32(&B->raw_free[s]), kConvWarps);
       mbar_init(smem_u32(&B->v_ready[s]), kConvWarps);
     }
+    for (int s = 0; s < 3; ++s) mbar_init(smem_u32(&B->v_empty[s]), 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(smem_u32(&B->v_empty[w]), 1);
       mbar_init(smem_u32(&B->s_full[w]), 1);
       mbar_init(smem_u32(&B->p_ready[w]), 4);
     }
