@@ -52,7 +52,7 @@
 // takes the clock from 1,965 to ~1,500 MHz); else a row tile's chain softmax ->
 // PV -> S -> softmax, 4,400 cycles over two streams, ~2,200 a step where the MMAs
 // alone take 1,024 and the exponentials (16 a clock) 1,024 (30 nodes, E4M3, 100,000
-// tokens: 73 us; 64 nodes, batch of 4: 124 us).  A launch's first and last 4 to 5 us
+// tokens: 73 to 75 us; 64 nodes, batch of 4: 124 to 128 us).  A launch's first and last 4 to 5 us
 // are set-up, the first tile, the end of the item and the join.
 #include <math.h>
 
