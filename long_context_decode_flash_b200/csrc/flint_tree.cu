@@ -968,6 +968,10 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   float a0 = 1.f, a1 = 0.f;
   int first = 0, chunks = 8;  // of 16 dims
   if (!two) {
+    // The exchange is the item's before until all eight warps have read it there,
+    // which their arrivals at that item's end tell.  (Nothing else orders the two:
+    // this item's first S does not wait for that end, and a stream may have no step.)
+    if (it.i > 0 && !warp_wait(smem_u32(&B->o_free), static_cast<uint32_t>(it.i - 1) & 1u, B)) return false;
     float2* ex = reinterpret_cast<float2*>(smem + Y::kEx);
     ex[w * kTrRows + r] = make_float2(m, l);
     __syncwarp();
