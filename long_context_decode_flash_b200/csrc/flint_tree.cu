@@ -330,6 +330,18 @@ __device__ __forceinline__ bool arm(int c, int size, uint64_t* gone, uint64_t* f
   return true;
 }
 
+// Waits until tile c of the ring of `size` has landed, for a warp that may not have
+// waited for the stage's tile before, c - size.  While that one is in flight its
+// parity reads as if c had landed, so its consumption comes first: one wait, then
+// the other.  (Two tests issued together are not answered in order: the first may
+// block while the second is answered.)  All of c - 2 size is consumed by then:
+// consumption goes in order, and a tile after c - size that the warp has met needed
+// one after c - 2 size consumed.
+__device__ __forceinline__ bool landed(int c, int size, Bars* B) {
+  if (c >= size && !warp_wait(smem_u32(&B->empty[c % size]), static_cast<uint32_t>(c / size - 1) & 1u, B)) return false;
+  return warp_wait(smem_u32(&B->full[c % size]), static_cast<uint32_t>(c / size) & 1u, B);
+}
+
 // A producer warp: K's (kV false) or V's tiles of the items, in order.  As the
 // MMA warp, it runs converged and elects the issuing lane (one warp for both
 // kinds took ~1,300 cycles a tile: the kernel's pace).  Page numbers are fetched 32
@@ -549,6 +561,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
       const int j = ct & 63;
       if (it.t0 == 0) {  // the drafts' K as the cache would hold it: codes, half a row a thread
         const int c = it.T;  // (the item's first K tile)
+        // (the stage's K tile before has landed: PV has passed the tile behind it)
         if (!raw_wait() || !warp_wait(smem_u32(&B->full[c % Y::kTiles]), static_cast<uint32_t>(c / Y::kTiles) & 1u, B)) return false;
         const uint8_t* from = raw_stage() + (ct >> 6) * kBox16 + j * 128;
         uint8_t* to = smem + Y::kTile + (c % Y::kTiles) * kCodes + j * 128;
@@ -642,7 +655,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
       } else {
         const int c = 2 * it.T + seq_of(true, tj, n, it.mt);
         tile = smem + Y::kTile + (c % Y::kTiles) * kStage;
-        if (!warp_wait(smem_u32(&B->full[c % Y::kTiles]), static_cast<uint32_t>(c / Y::kTiles) & 1u, B)) return false;
+        if (!landed(c, Y::kTiles, B)) return false;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint4 y[8];
