@@ -529,6 +529,9 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
   int raw = 0;  // E4M3: stages of codes and drafts read so far
   auto raw_stage = [&] { return smem + Y::kRaw + (raw % Y::kRaws) * kCodes; };
   auto raw_wait = [&] { return warp_wait(smem_u32(&B->raw_full[raw % Y::kRaws]), static_cast<uint32_t>(raw / Y::kRaws) & 1u, B); };
+  // (Behind the stores of what was made of the stage: a store needs its loads
+  // answered, an arrival does not.  Given back right behind the loads, stages were
+  // filled again before the last loads of a warp were answered.)
   auto raw_done = [&] {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&B->raw_free[raw % Y::kRaws]));
@@ -637,7 +640,6 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
         uint4 code[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) code[k] = smem4(raw_stage() + ct * 128 + ((k ^ ct) & 7) * 16);
-        raw_done();
         if (h > 0) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -652,6 +654,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
             smem4(tile + chunk_at(ct, 2 * k + 1)) = d;
           }
         }
+        raw_done();
       } else {
         const int c = 2 * it.T + seq_of(true, tj, n, it.mt);
         tile = smem + Y::kTile + (c % Y::kTiles) * kStage;
@@ -948,8 +951,9 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
     if (!warp_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, B)) return false;
     const int e = reinterpret_cast<const int8_t*>(smem + Y::kQExp)[(two ? w * kTrRows : 0) + r];
     scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&B->q_known));
+    // (an exponent is above -127: lane 0 arrives, once every lane's load is answered)
+    const bool none = __any_sync(0xffffffffu, e < -126);
+    if (lane == (none ? 1 : 0)) mbar_arrive(smem_u32(&B->q_known));
   }
   float m = -INFINITY, l = 0.f;  // m in log2 units, less P's bias
   for (int s = 0; s < steps; ++s) {

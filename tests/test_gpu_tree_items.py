@@ -30,7 +30,7 @@ def test_short_contexts_one_after_another(N, top, fp8):
             assert torch.equal(first.view(torch.int16), got.view(torch.int16))
 
 
-@pytest.mark.parametrize("fp8", [False])
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("lens,N", [([100_000], 40), ([60_000, 40_000, 70_001], 12), ([30_000] * 4, 33), ([100_000], 8)])
 def test_many_calls_back_to_back(lens, N, fp8):
     """Captured calls that follow one another without a pause, all SMs loading at
