@@ -460,7 +460,8 @@ size_t flint_tree_workspace_bytes(int32_t num_ctas);
  * its ancestors and itself, with the head's sink:
  *   out[b][i][h] = sum_j e^(s_j - M) V_j / (sum_j e^(s_j - M) + e^(sink_h - M)),
  *   s_j = q[b][i][h] . K_j / sqrt(128), M = max(max_j s_j, sink_h).
- * A chain (parent[i] = i - 1) gives what decoding its tokens one by one gives.
+ * A chain (parent[i] = i - 1) gives what decoding its tokens one by one gives, up
+ * to rounding.
  *   q         bf16 [B][N][32][128] (device, in), normed (and roped)
  *   k_draft, v_draft  bf16 [B][N][4][128] (device, in), final; with an E4M3
  *             cache they are attended as the cache would hold them (quantised
@@ -474,12 +475,18 @@ size_t flint_tree_workspace_bytes(int32_t num_ctas);
  *             rounded once; rows of nodes >= n_draft[b] are left as they were
  *   workspace device, >= flint_tree_workspace_bytes(num_ctas)
  * N in [1, FLINT_MAX_TREE], B in [1, FLINT_MAX_BATCH].  Scores and sums are
- * fp32; the probabilities and v enter their product in fp16 (v saturating at
- * +-65504, exact for bf16 values in the fp16 normal range, as in the
- * prefill).  With an E4M3 cache each row of q is held to 2^-17 of its largest
+ * fp32.  The probabilities enter their product with v in fp16, to 2^-11 of each
+ * or 2^-32 of the row's largest.  So does v: E4M3 values exactly, bf16 values
+ * exactly from 2^-14 to 65504 and to 2^-25 below.  A share of the keys that
+ * holds a bf16 v beyond (an infinite one too), or none of 2^-12, is done again
+ * in fp32 with v as it is: right for values of any size, but ~100 times as
+ * slow.  With an E4M3 cache each row of q is held to 2^-17 of its largest
  * magnitude, in two E4M3 terms.  Cache slots outside the attended range may
- * hold anything; a k or v that is NaN makes outputs NaN for the nodes that
- * attend it and leaves the others as they are.  Results are the same run to
+ * hold anything.  A k or v that is NaN makes outputs NaN for the nodes that
+ * attend it, an infinite bf16 v makes its dim infinite for them (NaN where its
+ * probability is 0 in fp32); both leave the others as they are.  An infinite
+ * drafted v against an E4M3 cache counts as the append would write it, 448
+ * times the scale.  Results are the same run to
  * run for given lengths, N, n_draft and num_ctas.  Paged block ids and time-outs as for
  * flint_attn_decode (nothing in the workspace needs zeroing after one). */
 flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const uint16_t* v_draft,

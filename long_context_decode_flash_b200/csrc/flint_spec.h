@@ -106,6 +106,9 @@ struct TreeParams {
   // [128 dims][32 | 4 heads][B * N nodes] bf16, boxes of 64 dims: 8 heads x 8
   // nodes, 1 head x 64 nodes
   CUtensorMap q_map, kd_map, vd_map;
+  // the same buffers by address (bf16; k and v: the cache's)
+  const uint16_t *q, *k_draft, *v_draft, *k, *v;
+  int64_t req_stride;          // elements
   const int32_t* parent;
   const float* sinks;
   uint16_t* out;

@@ -198,6 +198,12 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
   const size_t need = flint_tree_workspace_bytes(num_ctas);
   if (ws_bytes < need)
     return record_error(FLINT_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu needed", who, ws_bytes, need);
+  p.q = q;
+  p.k_draft = k_draft;
+  p.v_draft = v_draft;
+  p.k = static_cast<const uint16_t*>(c.k);
+  p.v = static_cast<const uint16_t*>(c.v);
+  p.req_stride = request_stride(c);
   p.parent = parent;
   p.sinks = sinks;
   p.out = out;

@@ -38,7 +38,10 @@
 // probabilities keep 11 bits down to 2^-21 of the largest and lose at most 2^-32
 // of it below (a bf16 P would round each by 2^-9; two bf16 terms made the softmax
 // and the PV product half as long again).  V is fp16 for it: exact for E4M3 and
-// for bf16 in fp16's normal range, saturating at 65504.  Against E4M3, K is the
+// for bf16 values from 2^-14 to 65504, to 2^-25 below.  An item (a share of a unit)
+// that holds a bf16 v beyond, or none of 2^-12 (so that 2^-25 would be more than
+// 2^-13 of the largest), is done again in fp32 after the CTA's last one
+// (exact_item).  Against E4M3, K is the
 // codes themselves and q two E4M3 terms a value (split_q_rows), at twice the MMA
 // rate of 16-bit operands.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).  P_w's fp16
@@ -111,7 +114,7 @@ struct Lay {
   static constexpr uint32_t kNan = kEx + 2 * kTrRows * 8;          // [kInfo][8] words
   static constexpr uint32_t kQExp = kNan + kInfo * 32;             // E4M3: exponents of Q's rows, int8 [2][128]
   static constexpr uint32_t kBar = kQExp + 2 * kTrRows;
-  static constexpr size_t kBytes = kBar + 384;
+  static constexpr size_t kBytes = kBar + 448;
 };
 static_assert(Lay<1, false>::kBytes <= 232448 && Lay<2, false>::kBytes <= 232448 && Lay<1, true>::kBytes <= 232448 &&
               Lay<2, true>::kBytes <= 232448, "shared memory of a CTA");
@@ -133,8 +136,10 @@ struct Bars {
   int abort;
   int q_armed;                           // items whose Q loads were issued
   int armed[6], raw_armed[4];            // per stage: 1 + the last tile armed, 0 for none
+  int odd;                               // bf16: some item is to be done again:
+  unsigned v_odd[kMaxTreeUnits / 32];    // ... these
 };
-static_assert(sizeof(Bars) <= 384, "barrier block");
+static_assert(sizeof(Bars) <= 448, "barrier block");
 
 // Instruction descriptors, fp32 D, M 128, N 128, A K-major; both operands bf16 or
 // both fp16 (kind::f16), or both E4M3 (kind::f8f6f4).  S: B (K) K-major; PV: B (V) dims-major.
@@ -221,13 +226,13 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// An fp16 pair with infinities made +-65504 and, where `clear`, NaN made 0;
-// any NaN sets `nan`.
-__device__ __forceinline__ uint32_t mend_pair(uint32_t x, bool clear, bool& nan) {
+// An fp16 pair, where `clear` with NaN made 0; any NaN sets `nan`, any infinity
+// `inf`.
+__device__ __forceinline__ uint32_t mend_pair(uint32_t x, bool clear, bool& nan, bool& inf) {
 #pragma unroll
   for (int e = 0; e < 32; e += 16) {
     const uint32_t mag = x >> e & 0x7FFFu;
-    if (mag == 0x7C00u) x -= 1u << e;
+    inf |= mag == 0x7C00u;
     if (mag > 0x7C00u) {
       nan = true;
       if (clear) x &= ~(0xFFFFu << e);
@@ -464,8 +469,25 @@ __device__ __forceinline__ uint32_t nan_acc(uint32_t acc, uint4 x) {
   return acc;
 }
 
-__device__ __forceinline__ uint4 mend(uint4 v, bool clear, bool& nan) {
-  return make_uint4(mend_pair(v.x, clear, nan), mend_pair(v.y, clear, nan), mend_pair(v.z, clear, nan), mend_pair(v.w, clear, nan));
+__device__ __forceinline__ uint4 mend(uint4 v, bool clear, bool& nan, bool& inf) {
+  return make_uint4(mend_pair(v.x, clear, nan, inf), mend_pair(v.y, clear, nan, inf), mend_pair(v.z, clear, nan, inf),
+                    mend_pair(v.w, clear, nan, inf));
+}
+// Per half of acc: the larger of it and the magnitudes of x (fp16), NaN if one is.
+constexpr uint32_t kSmallV = 0x0C00u;      // fp16 2^-12
+__device__ __forceinline__ void once_more(Bars* B, int item) {
+  atomicOr(&B->v_odd[item >> 5], 1u << (item & 31));
+  *reinterpret_cast<volatile int*>(&B->odd) = 1;
+}
+__device__ __forceinline__ uint32_t max_acc(uint32_t acc, uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t a;
+    asm("abs.f16x2 %0, %1;" : "=r"(a) : "r"(w[k]));
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(acc) : "r"(a));
+  }
+  return acc;
 }
 
 // A warp's 32 rows of a Q tile, bf16, into two E4M3 terms in place: with 2^e the
@@ -541,6 +563,8 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
   for (bool more = any; more; more = next_item(p, q, it)) {
     const TreeUnit& un = p.unit[it.u];
     const int b = un.b, nd = un.nodes, n = it.t1 - it.t0;
+    uint32_t largest = 0;  // bf16: this thread's v of the item, fp16 magnitudes
+    bool met = false;      // bf16: there was one
     const uint32_t before = static_cast<uint32_t>(it.i - 1) & 1u;
     if (warp == 0) {
       if (it.i > 0 && !warp_wait(smem_u32(&B->q_empty), before, B)) return false;
@@ -630,7 +654,8 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
               e4m3x4_to_f16x2x2(a, z.x, z.y);
               e4m3x4_to_f16x2x2(d, z.z, z.w);
             }
-            z = mend(z, true, lost_half);
+            bool none;
+            z = mend(z, true, lost_half, none);
             smem4(tile + chunk_at(j, 8 * (ct >> 6) + i)) = z;
           }
           half_rows = __ballot_sync(0xffffffffu, lost_half);
@@ -667,22 +692,29 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             y[k] = token ? bf16x8_to_f16(y[k]) : make_uint4(0, 0, 0, 0);
-            bad = nan_acc(bad, y[k]);
+            bad = max_acc(bad, y[k]);
             smem4(tile + chunk_at(ct, 8 * x + k)) = y[k];
           }
         }
+        bad = max(bad & 0xFFFFu, bad >> 16);
+        if (bad < 0x7C00u) largest = max(largest, bad);
+        met |= token;
       }
-      if (bad & 0x7FFF7FFFu) {
-        // Infinities saturate.  NaN becomes 0 where some rows do not attend the
-        // key; the rows that do learn of it by the record.  (Where all do, it
-        // stays.)
+      if (FP8 ? (bad & 0x7FFF7FFFu) != 0u : bad >= 0x7C00u) {
+        // NaN becomes 0 where some rows do not attend the key; the rows that do
+        // learn of it by the record.  (Where all do, it stays.)  Infinities: the
+        // item is done again.
+        bool over = false;
 #pragma unroll 1
         for (int k = 0; k < 16; ++k) {
           bool nan = false;
-          smem4(tile + chunk_at(ct, k)) = mend(smem4(tile + chunk_at(ct, k)), scan, nan);
+          smem4(tile + chunk_at(ct, k)) = mend(smem4(tile + chunk_at(ct, k)), scan, nan, over);
           has |= nan && scan;
         }
+        if (over) once_more(B, it.u - p.cut[q].unit);
       }
+      if (!FP8 && tj == n - 1 && __any_sync(0xffffffffu, met) && !__any_sync(0xffffffffu, largest >= kSmallV))
+        once_more(B, it.u - p.cut[q].unit);
       const uint32_t word = __ballot_sync(0xffffffffu, has);
       if (lane == 0) {
         // words 0..3: the rows; 4, 5: the drafts' rows, their second halves
@@ -839,6 +871,18 @@ __device__ __forceinline__ unsigned long long tree_line(const TreeParams& p, int
   return from(line[0], line[1], node);
 }
 
+// (All lanes of a warp; rows behind the request's nodes are as its last one's.)
+__device__ __forceinline__ Row row_of_node(const TreeParams& p, int b, int n, int L, int node, int lane) {
+  Row row;
+  row.line = tree_line(p, b, n, min(node, n - 1), lane);
+  const int depth = __popcll(row.line) - 1;
+  row.lo = p.window > 0 ? max(0, L + depth - (p.window - 1)) : 0;
+  row.hi = L;
+  row.r0 = row.lo % kWindow;
+  row.r1 = row.r0 + max(0, L - row.lo);
+  return row;
+}
+
 // The mask of half h (of the unit) for a row.
 __device__ __forceinline__ unsigned long long half_mask(const TreeParams& p, const TreeUnit& un, const Row& row, int h) {
   if (h == 0) return row.line;
@@ -940,13 +984,7 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   const uint32_t* losts = reinterpret_cast<const uint32_t*>(smem + Y::kNan);
   const int steps = it.stream_steps(w);
 
-  Row row;
-  row.line = tree_line(p, b, n, min(node, n - 1), lane);
-  const int depth = __popcll(row.line) - 1;
-  row.lo = p.window > 0 ? max(0, L + depth - (p.window - 1)) : 0;
-  row.hi = L;
-  row.r0 = row.lo % kWindow;
-  row.r1 = row.r0 + max(0, L - row.lo);
+  const Row row = row_of_node(p, b, n, L, node, lane);
   if (FP8) {
     if (!warp_wait(smem_u32(&B->q_ready), static_cast<uint32_t>(it.i) & 1u, B)) return false;
     const int e = reinterpret_cast<const int8_t*>(smem + Y::kQExp)[(two ? w * kTrRows : 0) + r];
@@ -1049,6 +1087,171 @@ __device__ __forceinline__ bool softmax_item(const TreeParams& p, const Item& it
   return true;
 }
 
+// A node's share of an item once more, bf16, in fp32 throughout, by one warp: v of
+// any size counts as the formula has it, infinite and NaN as well.  First the
+// maximum and the sum of the keys' scores, then the product with probabilities that
+// are divided by the sum already (so that nothing passes the largest v).  A lane
+// holds 4 dims of the 8 heads' q and O; a key's 8 scores are summed over the lanes
+// so that a lane is left with one head's (head_of).  Bound by the latency of its
+// loads: 8 nodes at 100,000 tokens 7.2 ms where the product in fp16 takes 52 us, and
+// 92 us where all v are 0 (which is seen first).  It is for values that the caches
+// of trained models do not hold; calls without them take what they took without it
+// (52 us; 32 paged requests of 16 nodes 531 us).
+__device__ __forceinline__ int head_of(int lane) { return lane >> 2; }
+// The element offset of a half's first row of KV head g, in the drafts (half 0) or
+// in the cache, for a half that holds a token.
+__device__ __forceinline__ long long first_row(const TreeParams& p, const TreeUnit& un, int half, int g) {
+  if (half == 0) return (static_cast<long long>(un.b) * p.N * kKvHeads + g) * kDim;
+  const int s0 = un.base + (half - 1) * kHalf;
+  if (p.layout != FLINT_KV_PAGED) return un.b * p.req_stride + (static_cast<long long>(s0) * kKvHeads + g) * kDim;
+  const int blk = p.table[static_cast<long long>(un.b) * p.max_blocks + s0 / kBlock];
+  return (static_cast<long long>(blk >= 0 && blk < p.num_blocks ? blk : 0) * kBlock * kKvHeads + g) * kDim;
+}
+// Whether an item has a v that is not 0 (by the softmax warps together).
+__device__ __forceinline__ bool some_v(const TreeParams& p, const Item& it, int g, int warp, int lane) {
+  const TreeUnit& un = p.unit[it.u];
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (int half = 2 * it.t0 + warp; half < min(2 * it.t1, un.halves); half += kSoftWarps) {
+    const int s0 = un.base + (half - 1) * kHalf;
+    const int j0 = half > 0 ? max(0, un.lo - s0) : 0, j1 = half > 0 ? min(kHalf, un.hi - s0) : un.nodes;
+    const uint16_t* v = (half > 0 ? p.v : p.v_draft) + first_row(p, un, half, g) + 4 * lane;
+#pragma unroll 8
+    for (int j = j0; j < j1; ++j) {
+      const uint2 x = *reinterpret_cast<const uint2*>(v + j * (kKvHeads * kDim));
+      bits |= (x.x | x.y) & 0x7FFF7FFFu;
+    }
+  }
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(bits), "n"(kSoftWarps * 32)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void exact_node(const TreeParams& p, const Item& it, int q, int g, int node, int lane) {
+  const TreeUnit& un = p.unit[it.u];
+  const int b = un.b, h0 = 2 * it.t0, h1 = min(2 * it.t1, un.halves);
+  const Row row = row_of_node(p, b, un.nodes, un.len, node, lane);
+  // visit(k, v, i): the lane's dims of each attended key, in order
+  auto keys = [&](auto&& visit) {
+#pragma unroll 1
+    for (int half = h0; half < h1; ++half) {
+      const unsigned long long mask = half_mask(p, un, row, half);
+      if (!mask) continue;
+      const long long at = first_row(p, un, half, g) + 4 * lane;
+      const uint16_t *k = (half > 0 ? p.k : p.k_draft) + at, *v = (half > 0 ? p.v : p.v_draft) + at;
+#pragma unroll 1
+      for (int j = 0; j < kHalf; j += 2) {
+        uint2 kr[2], vr[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (mask >> (j + i) & 1) {
+            kr[i] = *reinterpret_cast<const uint2*>(k + (j + i) * (kKvHeads * kDim));
+            vr[i] = *reinterpret_cast<const uint2*>(v + (j + i) * (kKvHeads * kDim));
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (mask >> (j + i) & 1) visit(kr[i], vr[i]);
+      }
+    }
+  };
+  uint2 qr[kGroup];
+#pragma unroll
+  for (int h = 0; h < kGroup; ++h)
+    qr[h] = *reinterpret_cast<const uint2*>(p.q + ((static_cast<long long>(b) * p.N + node) * kHeads + g * kGroup + h) * kDim + 4 * lane);
+  // the score of the lane's head, in log2 units
+  auto score = [&](uint2 k) {
+    float s[kGroup];
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h)
+      s[h] = fmaf(bf16_lo(qr[h].x), bf16_lo(k.x), bf16_hi(qr[h].x) * bf16_hi(k.x)) + fmaf(bf16_lo(qr[h].y), bf16_lo(k.y), bf16_hi(qr[h].y) * bf16_hi(k.y));
+#pragma unroll
+    for (int o = 16, n = kGroup / 2; n > 0; o >>= 1, n >>= 1)
+#pragma unroll
+      for (int h = 0; h < n; ++h) {
+        const bool upper = (lane & o) != 0;
+        const float give = upper ? s[h] : s[h + n], keep = upper ? s[h + n] : s[h];
+        s[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+    return s[0] * kTrScale;
+  };
+  float m = -INFINITY, l = 0.f;
+  keys([&](uint2 k, uint2) {
+    const float x = score(k), top = fmaxf(m, x);
+    if (x != x) l = x;
+    if (top != -INFINITY) {
+      l = l * ex2(m - top) + ex2(x - top);
+      m = top;
+    }
+  });
+  const float inv = 1.f / l;
+  float o[kGroup][4];
+#pragma unroll
+  for (int h = 0; h < kGroup; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[h][i] = 0.f;
+  keys([&](uint2 k, uint2 v) {
+    const float mine = ex2(score(k) - m) * inv;
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h) {
+      const float pr = __shfl_sync(0xffffffffu, mine, 4 * h);
+      o[h][0] = fmaf(pr, bf16_lo(v.x), o[h][0]);
+      o[h][1] = fmaf(pr, bf16_hi(v.x), o[h][1]);
+      o[h][2] = fmaf(pr, bf16_lo(v.y), o[h][2]);
+      o[h][3] = fmaf(pr, bf16_hi(v.y), o[h][3]);
+    }
+  });
+  // whole: the sink's share off; else a partial with l in [1/2, 1)
+  const bool whole = it.whole(p);
+  int e = 0;
+  const float f = whole ? l / (l + ex2(p.sinks[g * kGroup + head_of(lane)] * kTrLog2e - m)) : frexpf(l, &e);
+  const int in_unit = node - un.rb * 2 * kTrNodes, r0 = (in_unit & (kTrNodes - 1)) * kGroup, slot = it.u == p.cut[q].unit ? 0 : 1;
+  float* part = p.partials + ((static_cast<long long>(q) * kKvHeads + g) * 4 + slot * 2 + (in_unit >> 4)) * kTreePartialFloats;
+#pragma unroll
+  for (int h = 0; h < kGroup; ++h) {
+    const float x = __shfl_sync(0xffffffffu, f, 4 * h);
+    const float4 y = make_float4(o[h][0] * x, o[h][1] * x, o[h][2] * x, o[h][3] * x);
+    if (whole)
+      reinterpret_cast<uint2*>(p.out + ((static_cast<long long>(b) * p.N + node) * kHeads + g * kGroup + h) * kDim)[lane] =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    else
+      reinterpret_cast<float4*>(part)[lane * kTrRows + r0 + h] = y;
+  }
+  if (!whole && (lane & 3) == 0) {
+    float* ml = part + kTrRows * kDim + r0 + head_of(lane);
+    ml[0] = m + static_cast<float>(e);
+    ml[kTrRows] = f;
+    if (un.dup == 2) {  // the second copy of the row: nothing (O is 0 times it)
+      ml[kTrRows / 2] = -INFINITY;
+      ml[kTrRows + kTrRows / 2] = 0.f;
+    }
+  }
+  if (!whole && un.dup == 2)
+#pragma unroll
+    for (int h = 0; h < kGroup; ++h) reinterpret_cast<float4*>(part)[lane * kTrRows + kTrRows / 2 + r0 + h] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// After a CTA's last item (bf16): those whose v left fp16's range, a node a warp.
+// (Not inlined: the code that every call runs stays short.)
+__device__ __noinline__ void exact_items(const TreeParams& p, int q, int g, const Bars* B, int warp, int lane) {
+  const int u0 = p.cut[q].unit;
+  const volatile unsigned* odd = B->v_odd;
+  Item it;
+  it.u = u0;
+  it.t0 = p.cut[q].tile;
+#pragma unroll 1
+  for (; clip(p, q, it); ++it.u, it.t0 = 0) {
+    if (!(odd[(it.u - u0) >> 5] >> ((it.u - u0) & 31) & 1u) || !some_v(p, it, g, warp, lane)) continue;  // (of 0 alone O is 0 already)
+    const int first = p.unit[it.u].rb * 2 * kTrNodes, end = min(first + 2 * kTrNodes, static_cast<int>(p.unit[it.u].nodes));
+#pragma unroll 1
+    for (int node = first + warp; node < end; node += kSoftWarps) exact_node(p, it, q, g, node, lane);
+  }
+}
+
 template <int MT, bool FP8>
 __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1089,6 +1292,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
     mbar_init(smem_u32(&B->o_full), 1);
     mbar_init(smem_u32(&B->o_free), kSoftWarps);
     mbar_init(smem_u32(&B->ex_full), kSoftWarps);
+    for (int k = 0; k < kMaxTreeUnits / 32; ++k) B->v_odd[k] = 0;
+    B->odd = 0;
     mbar_init(smem_u32(&B->mma_done), 1);
     B->abort = 0;
     B->q_armed = 0;
@@ -1133,6 +1338,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  if (!FP8 && *reinterpret_cast<const volatile int*>(&B->odd) && warp < kSoftWarps && !aborted(B)) exact_items(p, q, g, B, warp, lane);
   if (warp == kTmaWarp && lane == 0 && aborted(B)) {
     // copies in flight land before the CTA's shared memory goes away: Q and the
     // last of each stage (an earlier one was consumed, so it landed)
@@ -1207,6 +1413,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     for (int k = lane; k < parts; k += 32) M = max3_nan(M, wt[k][wr].x, wt[k][wr].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = max3_nan(M, __shfl_xor_sync(0xffffffffu, M, o), M);
+    M += 8.0f;  // (so that up to 2^8 partials of the largest bf16 sum to something finite)
     float l = 0.f;
     for (int k = lane; k < parts; k += 32) {
       const float2 ml = wt[k][wr];
