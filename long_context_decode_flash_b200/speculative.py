@@ -2,8 +2,14 @@
 batch stand as a tree on each request's committed context; every layer norms
 and rotates them at their positions and attends the cache and the tree
 (attend_layer), and once the target's probabilities are known the accepted
-path is found and written to every layer's cache (verify_and_append).  Nothing
-here waits for the GPU: the accepted counts stay on the device.
+path is found and written to every layer's cache (verify_and_append).
+
+From the first layer to the append nothing waits for the GPU: the accepted
+counts stay on the device.  Lengths and node counts are host values that go into
+the launches, so the next step has to read n_accepted, and a captured step holds
+for the lengths that it was captured with.  A loop that keeps the drafted k and v
+of its layers in buffers of its own (attend_layer's k) builds the layers' array,
+flint.path_layers, once.
 
 This module only marshals: the compute steps run in the CUDA library."""
 from __future__ import annotations
@@ -45,17 +51,24 @@ class DraftTree:
 
 def attend_layer(tree: DraftTree, pos: torch.Tensor, q_raw: torch.Tensor, k_raw: torch.Tensor, v: torch.Tensor,
                  w_q, w_k, rope: Optional[flint.Rope], cache: flint.KVCache, seq_lens: Sequence[int], sinks, window: int,
-                 ws: torch.Tensor, eps: float = 1e-6, dev_err=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                 ws: torch.Tensor, eps: float = 1e-6, dev_err=None, k: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One layer of the step: q_raw [B, N, 32, 128], k_raw and v [B, N, 4, 128] in
     bf16 (q_raw and k_raw may be slices of a fused projection's rows).  Returns
-    (out bf16 [B, N, 32, 128], the drafted k after norm and rotation)."""
+    (out bf16 [B, N, 32, 128], the drafted k after norm and rotation bf16
+    [B, N, 4, 128]), in the caller's dense buffers where these are given.  Rows of
+    out behind a request's nodes are 0, in a given buffer as they were."""
     B, N = pos.shape
     q = torch.empty((B, N, flint.NUM_Q_HEADS, flint.HEAD_DIM), dtype=torch.bfloat16, device=pos.device)
-    k = torch.empty((B, N, flint.NUM_KV_HEADS, flint.HEAD_DIM), dtype=torch.bfloat16, device=pos.device)
+    if k is None:
+        k = torch.empty((B, N, flint.NUM_KV_HEADS, flint.HEAD_DIM), dtype=torch.bfloat16, device=pos.device)
+    elif k.shape != (B, N, flint.NUM_KV_HEADS, flint.HEAD_DIM) or not k.is_contiguous():
+        raise ValueError(f"k must be a dense tensor [{B}, {N}, {flint.NUM_KV_HEADS}, {flint.HEAD_DIM}]")
     flint.flint_qk_norm_rope_at(q_raw.flatten(0, 1), k_raw.flatten(0, 1), w_q, w_k, pos.reshape(-1), rope, eps,
                                 q_out=q.view(B * N, flint.NUM_Q_HEADS, flint.HEAD_DIM),
                                 k_out=k.view(B * N, flint.NUM_KV_HEADS, flint.HEAD_DIM))
-    out = torch.zeros_like(q)
+    if out is None:
+        out = torch.zeros_like(q)
     flint.flint_attn_tree(q, k, v, tree.parent, cache, seq_lens, tree.n_draft, sinks, window, out, ws, dev_err=dev_err)
     return out, k
 
