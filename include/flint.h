@@ -519,7 +519,8 @@ flint_status flint_attn_tree(const uint16_t* q, const uint16_t* k_draft, const u
  *   path    device int32 [B][N] (out): the accepted nodes in order, then -1
  *   n_accepted, next_token  device int32 [B] (out)
  * N in [1, FLINT_MAX_TREE], B in [1, FLINT_MAX_BATCH].  All arithmetic in
- * double: a draw that decides at a border decides as the formula does. */
+ * double, the sums in an order of their own: only a draw within their rounding
+ * of a border may fall on its other side.  Results are the same run to run. */
 flint_status flint_verify_tree(const float* target, int64_t target_stride, const float* draft,
                                int64_t draft_stride, const int32_t* tokens, const int32_t* parent,
                                const int32_t* n_draft, int32_t B, int32_t N, int32_t V,
