@@ -114,13 +114,16 @@ struct Lay {
   static constexpr uint32_t kNan = kEx + 2 * kTrRows * 8;          // [kInfo][8] words
   static constexpr uint32_t kQExp = kNan + kInfo * 32;             // E4M3: exponents of Q's rows, int8 [2][128]
   static constexpr uint32_t kBar = kQExp + 2 * kTrRows;
-  static constexpr size_t kBytes = kBar + 448;
+  static constexpr size_t kBytes = kBar + 512;
 };
 static_assert(Lay<1, false>::kBytes <= 232448 && Lay<2, false>::kBytes <= 232448 && Lay<1, true>::kBytes <= 232448 &&
               Lay<2, true>::kBytes <= 232448, "shared memory of a CTA");
 
 struct Bars {
-  uint64_t full[6], empty[6];            // a tile (E4M3: K tile) landed; was consumed
+  uint64_t full[6], empty[6];            // a K tile landed; a tile (E4M3: K tile) was consumed
+  // bf16: a V tile landed.  (Apart from K's: a parity tells a phase from its
+  // neighbours only, and who waits for V tiles does not wait for the K tiles between.)
+  uint64_t full_v[6];
   uint64_t raw_full[4], raw_free[4];     // E4M3: V's codes, or drafts, landed; were read
   uint64_t v_empty[3];                   // E4M3: an fp16 V tile was consumed
   uint64_t v_ready[4];                   // V of tile T (mod 4) is an operand
@@ -135,11 +138,11 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
   int q_armed;                           // items whose Q loads were issued
-  int armed[6], raw_armed[4];            // per stage: 1 + the last tile armed, 0 for none
+  int armed[6], armed_v[6], raw_armed[4];  // per barrier: phases armed
   int odd;                               // bf16: some item is to be done again:
   unsigned v_odd[kMaxTreeUnits / 32];    // ... these
 };
-static_assert(sizeof(Bars) <= 448, "barrier block");
+static_assert(sizeof(Bars) <= 512, "barrier block");
 
 // Instruction descriptors, fp32 D, M 128, N 128, A K-major; both operands bf16 or
 // both fp16 (kind::f16), or both E4M3 (kind::f8f6f4).  S: B (K) K-major; PV: B (V) dims-major.
@@ -329,22 +332,10 @@ __device__ __forceinline__ bool elect() {
 __device__ __forceinline__ bool arm(int c, int size, uint64_t* gone, uint64_t* full, int* armed, uint32_t bytes, Bars* B) {
   if (c >= size && !warp_wait(smem_u32(&gone[c % size]), static_cast<uint32_t>(c / size - 1) & 1u, B)) return false;
   if (elect()) {
-    armed[c % size] = c + 1;
+    ++armed[c % size];
     mbar_expect_tx(smem_u32(&full[c % size]), bytes);
   }
   return true;
-}
-
-// Waits until tile c of the ring of `size` has landed, for a warp that may not have
-// waited for the stage's tile before, c - size.  While that one is in flight its
-// parity reads as if c had landed, so its consumption comes first: one wait, then
-// the other.  (Two tests issued together are not answered in order: the first may
-// block while the second is answered.)  All of c - 2 size is consumed by then:
-// consumption goes in order, and a tile after c - size that the warp has met needed
-// one after c - 2 size consumed.
-__device__ __forceinline__ bool landed(int c, int size, Bars* B) {
-  if (c >= size && !warp_wait(smem_u32(&B->empty[c % size]), static_cast<uint32_t>(c / size - 1) & 1u, B)) return false;
-  return warp_wait(smem_u32(&B->full[c % size]), static_cast<uint32_t>(c / size) & 1u, B);
 }
 
 // A producer warp: K's (kV false) or V's tiles of the items, in order.  As the
@@ -417,8 +408,8 @@ __device__ __forceinline__ bool run_tma(const TreeParams& p, int q, int g, uint3
         if (kV) ++raws;
       } else {
         const int c = 2 * it.T + seq_of(kV, j, n, it.mt);
-        if (!arm(c, Y::kTiles, B->empty, B->full, B->armed, (boxes + (h == 0 ? 1u : 0u)) * 2 * kBox16, B)) return false;
-        const uint32_t bar = smem_u32(&B->full[c % Y::kTiles]), dst = base + Y::kTile + (c % Y::kTiles) * kStage;
+        if (!arm(c, Y::kTiles, B->empty, kV ? B->full_v : B->full, kV ? B->armed_v : B->armed, (boxes + (h == 0 ? 1u : 0u)) * 2 * kBox16, B)) return false;
+        const uint32_t bar = smem_u32(&(kV ? B->full_v : B->full)[c % Y::kTiles]), dst = base + Y::kTile + (c % Y::kTiles) * kStage;
         if (elect()) {
           if (box0) {
             tma_load_4d(dst, map, bar, 0, g, row0, req0);
@@ -549,6 +540,7 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
   using Y = Lay<MT, FP8>;
   const int lane = ct & 31, warp = ct >> 5;
   int raw = 0;  // E4M3: stages of codes and drafts read so far
+  uint32_t phases = 0;  // bf16: the parity of each stage's next V tile
   auto raw_stage = [&] { return smem + Y::kRaw + (raw % Y::kRaws) * kCodes; };
   auto raw_wait = [&] { return warp_wait(smem_u32(&B->raw_full[raw % Y::kRaws]), static_cast<uint32_t>(raw / Y::kRaws) & 1u, B); };
   // (Behind the stores of what was made of the stage: a store needs its loads
@@ -683,7 +675,8 @@ __device__ __forceinline__ bool run_conv(const TreeParams& p, int q, int g, uint
       } else {
         const int c = 2 * it.T + seq_of(true, tj, n, it.mt);
         tile = smem + Y::kTile + (c % Y::kTiles) * kStage;
-        if (!landed(c, Y::kTiles, B)) return false;
+        if (!warp_wait(smem_u32(&B->full_v[c % Y::kTiles]), phases >> (c % Y::kTiles) & 1u, B)) return false;
+        phases ^= 1u << (c % Y::kTiles);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint4 y[8];
@@ -740,6 +733,7 @@ template <int MT, bool FP8>
 __device__ __forceinline__ void run_mma(const TreeParams& p, int q, uint32_t base, uint32_t tmem, Bars* B, int lane, bool any, const Item& it0) {
   using Y = Lay<MT, FP8>;
   bool ok = true;
+  uint32_t phases = 0;  // bf16: the parity of each stage's next K tile
   Item it = it0;
   for (bool more = any; ok && more; more = next_item(p, q, it)) {
     const int n = it.t1 - it.t0, two = it.mt == 2;
@@ -751,7 +745,7 @@ __device__ __forceinline__ void run_mma(const TreeParams& p, int q, uint32_t bas
       // step s2's K tile
       const bool more_s = s2 < it.steps;
       const int tk = two ? s2 >> 1 : s2, ck = FP8 ? it.T + tk : 2 * it.T + seq_of(false, tk, n, it.mt), sk = ck % Y::kTiles;
-      const uint32_t k_bar = smem_u32(&B->full[sk]), k_par = static_cast<uint32_t>(ck / Y::kTiles) & 1u;
+      const uint32_t k_bar = smem_u32(&B->full[sk]), k_par = FP8 ? static_cast<uint32_t>(ck / Y::kTiles) & 1u : phases >> sk & 1u;
       bool k_ok = !more_s || mbar_try_wait(k_bar, k_par);
       if (s >= 0) {
         const int tv = two ? s >> 1 : s, T = it.T + tv, cv = 2 * it.T + seq_of(true, tv, n, it.mt), sv = cv % Y::kTiles;
@@ -784,6 +778,7 @@ __device__ __forceinline__ void run_mma(const TreeParams& p, int q, uint32_t bas
           ok = warp_wait(k_bar, k_par, B);
           if (!ok) break;
         }
+        if (!FP8 && (!two || w)) phases ^= 1u << sk;
         tc_fence_after();
         // S = Q K^T: 16 dims per MMA, or 32 in each of Q's two E4M3 terms
         const uint64_t qd = sw128_desc(base + (two ? w * kQTile : 0), 16, 1024);
@@ -1269,8 +1264,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      B->armed[s] = 0;
+      B->armed[s] = B->armed_v[s] = 0;
       mbar_init(smem_u32(&B->full[s]), 1);
+      mbar_init(smem_u32(&B->full_v[s]), 1);
       mbar_init(smem_u32(&B->empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) {
@@ -1348,10 +1344,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const __grid_consta
         if (globaltimer_ns() - t0 > kWaitLimitNs) break;
     };
     if (B->q_armed > 0) land(&B->q_full, B->q_armed - 1);
-    for (int st = 0; st < Y::kTiles; ++st)
-      if (B->armed[st] > 0) land(&B->full[st], (B->armed[st] - 1) / Y::kTiles);
+    for (int st = 0; st < Y::kTiles; ++st) {
+      if (B->armed[st] > 0) land(&B->full[st], B->armed[st] - 1);
+      if (B->armed_v[st] > 0) land(&B->full_v[st], B->armed_v[st] - 1);
+    }
     for (int st = 0; st < Y::kRaws; ++st)
-      if (B->raw_armed[st] > 0) land(&B->raw_full[st], (B->raw_armed[st] - 1) / Y::kRaws);
+      if (B->raw_armed[st] > 0) land(&B->raw_full[st], B->raw_armed[st] - 1);
   }
   if (warp == kMmaWarp) {
     __syncwarp();
