@@ -39,23 +39,22 @@
 // of it below (a bf16 P would round each by 2^-9; two bf16 terms made the softmax
 // and the PV product half as long again).  V is fp16 for it: exact for E4M3 and
 // for bf16 values from 2^-14 to 65504, to 2^-25 below.  An item (a share of a unit)
-// that holds a bf16 v beyond, or none of 2^-12 (so that 2^-25 would be more than
-// 2^-13 of the largest), is done again in fp32 after the CTA's last one
-// (exact_item).  Against E4M3, K is the
-// codes themselves and q two E4M3 terms a value (split_q_rows), at twice the MMA
-// rate of 16-bit operands.
+// that holds a bf16 v beyond, or where a converter warp met none of 2^-12 (so that
+// 2^-25 could be more than 2^-13 of the largest), is done again in fp32 after the
+// CTA's last one (exact_items).  Against E4M3, K is the codes themselves and q two
+// E4M3 terms a value (split_q_rows), at twice the MMA rate of 16-bit operands.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).  P_w's fp16
 // pairs lie over S_w: those of keys 32 k .. 32 k + 31 at columns 32 k ..  32 k + 15.
 // Every wait is bounded; a timeout raises FLINT_ERR_TIMEOUT.
 //
 // What bounds it, and what it measured (one B200, launches back to back; a tile is
 // 128 keys): up to 16 nodes on a bf16 cache the bytes (8 nodes at 100,000 tokens
-// 51 us, of which 31 us are the cache's 205 MB; 32 requests of up to 16 nodes
-// 468 us in a burst for 2.65 GB, 5.7 TB/s, and 570 us sustained, when the power limit
-// takes the clock from 1,965 to ~1,500 MHz); else a row tile's chain softmax ->
+// 50 to 51 us, of which 31 us are the cache's 205 MB; 32 requests of up to 16 nodes
+// 510 us in a burst for 2.65 GB, 5.2 TB/s, and 600 us sustained, when the power limit
+// takes the clock from 1,965 to 1,537 MHz); else a row tile's chain softmax ->
 // PV -> S -> softmax, 4,400 cycles over two streams, ~2,200 a step where the MMAs
 // alone take 1,024 and the exponentials (16 a clock) 1,024 (30 nodes, E4M3, 100,000
-// tokens: 73 to 75 us; 64 nodes, batch of 4: 124 to 128 us).  A launch's first and last 4 to 5 us
+// tokens: 72 to 75 us; 64 nodes, batch of 4: 122 to 127 us).  A launch's first and last 4 to 5 us
 // are set-up, the first tile, the end of the item and the join.
 #include <math.h>
 

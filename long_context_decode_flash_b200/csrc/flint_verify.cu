@@ -15,10 +15,10 @@
 // cluster's shared memory, and every thread walks on with the same totals.  The
 // shares' sums also tell which share holds the drawn token: its CTA alone reads
 // it again.  Bound by the rows' loads for large batches (64 chains of
-// 6 over 150,001 tokens: 69 MB at 4.9 TB/s for 14 us of the 25; three times as many
+// 6 over 150,001 tokens: 69 MB at 4.9 TB/s for 14 us of the 22 to 25; three times as many
 // loads in flight measured no faster), and else by the steps in turn: launch 2 us,
 // the gathers 1 to 2 us, a pass over a row 1.5 to 3 us, the draw 1 to 4 us (one
-// chain of 4: 6.8 us; 16 trees of 31: 13.7 us).
+// chain of 4: 6.2 to 6.9 us; 16 trees of 31: 12 to 14 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
